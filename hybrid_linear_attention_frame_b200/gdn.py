@@ -24,7 +24,10 @@ EXPORTS = ("gdn_forward", "gdn_state_step", "gdn_forward_f32", "gdn_state_step_f
            "gdn_forward_host_ws", "gdn_forward_static_ws", "gdn_forward_gated",
            "gdn_forward_gated_f32", "gdn_bidir_workspace_bytes", "gdn_forward_bidir",
            "gdn_forward_bidir_f32", "gdn_forward_fp8", "gdn_softmax_attention", "gdn_set_wait_limit_ns", "gdn_status_string",
-           "gdn_get_last_device_status", "gdn_bf16_path", "gdn_version")
+           "gdn_get_last_device_status", "gdn_bf16_path", "gdn_version",
+           "gdn_causal_conv", "gdn_causal_conv_f32", "gdn_causal_conv_step", "gdn_causal_conv_step_f32",
+           "gdn_selective_scan", "gdn_selective_scan_f32", "gdn_selective_scan_step", "gdn_selective_scan_step_f32",
+           "gdn_window_attention", "gdn_window_cache_append", "gdn_window_attention_step")
 
 
 class GdnError(RuntimeError):

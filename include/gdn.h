@@ -53,8 +53,10 @@
  * (gdn_forward_ws, gdn_state_step_ws, gdn_forward_host_ws, gdn_forward_static_ws),
  * the other gate placement (gdn_forward_gated*), the bidirectional form of the
  * dense checkpoint (gdn_forward_bidir*), the chunk-causal softmax attention layer
- * with its rolling KV cache (gdn_softmax_attention), and the status and wait-bound
- * controls (gdn_get_last_device_status, gdn_set_wait_limit_ns).
+ * with its rolling KV cache (gdn_softmax_attention), the other sequence mixers of a
+ * hybrid stack (gdn_causal_conv*, gdn_selective_scan*, gdn_window_attention* and its
+ * cache), and the status and wait-bound controls (gdn_get_last_device_status,
+ * gdn_set_wait_limit_ns).
  */
 #ifndef GDN_H
 #define GDN_H
@@ -342,6 +344,155 @@ int gdn_softmax_attention(const void* q, const void* k, const void* v, void* out
                           int B, int H, int T, int d_k, int d_v,
                           int frame_len, int frames_per_block, int cached_blocks, int sink_frames,
                           cudaStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The other sequence mixers of a hybrid stack, token by token: the short causal
+ * convolution in front of a recurrent mixer, the selective state space scan, and
+ * softmax attention over a sliding window with sink tokens.  Each has a call for a
+ * prompt (or a streaming block) and one for the next token of every session; the
+ * state or cache carries a session from one call to the next.
+ *
+ * Common to them.  Element type bf16 (the *_f32 entries: float32); weights and
+ * states as declared.  *_stride arguments are in elements, so that an activation
+ * may be a slice of a projection's wider rows: row t of batch entry b starts at
+ * p + b * batch_stride + t * row_stride, its elements contiguous.  Every tensor's
+ * base must be 16-byte aligned and its strides multiples of 16 bytes; a stride
+ * over a dimension of size 1 is not looked at.  Outputs, states and caches are
+ * contiguous.  `lengths` (device, int32 [B], may be NULL) gives the number of
+ * valid tokens of each sequence of a padded batch, clamped to [0, T]: rows at and
+ * past it are not read into any result and their outputs are left as they were.
+ * Work goes to `stream`, one kernel launch per call, no workspace, no allocation,
+ * no host synchronisation; the calls can be captured into graphs, and calls in
+ * flight on several streams share nothing but the caller's buffers.  Arguments
+ * are checked on the host first (GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED;
+ * nothing is enqueued on an error); an output or state may not overlap an input,
+ * except a state updated in place.  With no token (T, Tq = 0) the per-token tensors
+ * may be NULL.  B <= 65535.
+ */
+
+/*
+ * Causal depthwise convolution of width 2, 3 or 4:
+ *     out[b, t, c] = act(bias[c] + sum_j weight[c, j] x[b, t - width + 1 + j, c]),
+ * act = SiLU (silu = 1) or none (0); accumulated in fp32, rounded once.
+ *   x          [B, T, D] through strides; out [B, T, D]
+ *   weight     [D, width] float32; bias [D] float32 or NULL
+ *   state_in   [B, width - 1, D], element type of x: the inputs before the call's
+ *              first token, oldest first; NULL: zeros
+ *   state_out  the same after each sequence's last valid token, or NULL; may be
+ *              state_in.  T = 0 carries the state over.
+ * D a multiple of 8.  gdn_causal_conv_step: T = 1, the state in place.
+ */
+int gdn_causal_conv(const void* x, long long x_batch_stride, long long x_row_stride,
+                    const float* weight, const float* bias, const void* state_in, void* state_out,
+                    const int* lengths, void* out, int B, int T, int D, int width, int silu, cudaStream_t stream);
+
+int gdn_causal_conv_f32(const float* x, long long x_batch_stride, long long x_row_stride,
+                        const float* weight, const float* bias, const float* state_in, float* state_out,
+                        const int* lengths, float* out, int B, int T, int D, int width, int silu, cudaStream_t stream);
+
+int gdn_causal_conv_step(const void* x, long long x_batch_stride, const float* weight, const float* bias,
+                         void* state, void* out, int B, int D, int width, int silu, cudaStream_t stream);
+
+int gdn_causal_conv_step_f32(const float* x, long long x_batch_stride, const float* weight, const float* bias,
+                             float* state, float* out, int B, int D, int width, int silu, cudaStream_t stream);
+
+/*
+ * Selective state space scan.  Per batch entry and channel d, with N states:
+ *     delta_t = dt_t + dt_bias[d], through softplus when dt_softplus = 1,
+ *     h_t[n]  = exp(delta_t A[d, n]) h_{t-1}[n] + delta_t x_t Bm_t[n],
+ *     y_t     = (sum_n Cm_t[n] h_t[n] + skip[d] x_t) silu(z_t).
+ *   x, dt, z   [B, T, D] through strides (z may be NULL: no gate); y [B, T, D]
+ *   Bm, Cm     [B, T, N] through strides, shared by all channels
+ *   A          [D, N] float32, as it stands in the exponent (usually negative)
+ *   skip, dt_bias   [D] float32 or NULL (0)
+ *   state_in   [B, D, N] float32 or NULL (zeros); state_out the state after each
+ *              sequence's last valid token, or NULL; may be state_in
+ * N = 8, 16, 32 or 64; D a multiple of 8.  The state and all sums are fp32; y is
+ * rounded once.  T = 0 carries the state over.  gdn_selective_scan_step: T = 1,
+ * the state in place.
+ */
+int gdn_selective_scan(const void* x, long long x_batch_stride, long long x_row_stride,
+                       const void* dt, long long dt_batch_stride, long long dt_row_stride,
+                       const float* A,
+                       const void* Bm, long long b_batch_stride, long long b_row_stride,
+                       const void* Cm, long long c_batch_stride, long long c_row_stride,
+                       const float* skip, const void* z, long long z_batch_stride, long long z_row_stride,
+                       const float* dt_bias, const float* state_in, float* state_out, const int* lengths, void* y,
+                       int B, int T, int D, int N, int dt_softplus, cudaStream_t stream);
+
+int gdn_selective_scan_f32(const float* x, long long x_batch_stride, long long x_row_stride,
+                           const float* dt, long long dt_batch_stride, long long dt_row_stride,
+                           const float* A,
+                           const float* Bm, long long b_batch_stride, long long b_row_stride,
+                           const float* Cm, long long c_batch_stride, long long c_row_stride,
+                           const float* skip, const float* z, long long z_batch_stride, long long z_row_stride,
+                           const float* dt_bias, const float* state_in, float* state_out, const int* lengths, float* y,
+                           int B, int T, int D, int N, int dt_softplus, cudaStream_t stream);
+
+int gdn_selective_scan_step(const void* x, long long x_batch_stride, const void* dt, long long dt_batch_stride,
+                            const float* A, const void* Bm, long long b_batch_stride,
+                            const void* Cm, long long c_batch_stride, const float* skip,
+                            const void* z, long long z_batch_stride, const float* dt_bias, float* state, void* y,
+                            int B, int D, int N, int dt_softplus, cudaStream_t stream);
+
+int gdn_selective_scan_step_f32(const float* x, long long x_batch_stride, const float* dt, long long dt_batch_stride,
+                                const float* A, const float* Bm, long long b_batch_stride,
+                                const float* Cm, long long c_batch_stride, const float* skip,
+                                const float* z, long long z_batch_stride, const float* dt_bias, float* state, float* y,
+                                int B, int D, int N, int dt_softplus, cudaStream_t stream);
+
+/*
+ * Sliding-window softmax attention with sinks.  Query i of a call is token
+ * t = Tk - Tq + i of its sequence (the queries are the last Tq of the Tk tokens in
+ * k and v: Tq = Tk is a whole prompt, Tq < Tk its next piece):
+ *     out_i = sum_{s in K(t)} softmax_s(scale q_i . k_s) v_s,
+ *     K(t) = {s <= t : s > t - window or s < sinks}.
+ * Query heads share key heads in order: head h reads key head h / (Hq / Hkv).
+ *   q [B, Tq, Hq, d_k], k [B, Tk, Hkv, d_k], v [B, Tk, Hkv, d_v] bf16, each through
+ *   batch, row and head strides (so [B, H, T, d] tensors fit too); out
+ *   [B, Tq, Hq, d_v] bf16.  With `lengths` a query past its sequence's length is
+ *   padding: its row of out is left as it was.
+ * Hq a multiple of Hkv; d_k, d_v multiples of 16 in 16..128; window >= 1,
+ * sinks >= 0, scale > 0 and finite.  Scores and the softmax in fp32, the weights
+ * rounded to bf16 for their product with v, out rounded once.
+ */
+int gdn_window_attention(const void* q, long long q_batch_stride, long long q_row_stride, long long q_head_stride,
+                         const void* k, long long k_batch_stride, long long k_row_stride, long long k_head_stride,
+                         const void* v, long long v_batch_stride, long long v_row_stride, long long v_head_stride,
+                         const int* lengths, void* out, int B, int Tq, int Tk, int Hq, int Hkv, int d_k, int d_v,
+                         int window, int sinks, float scale, cudaStream_t stream);
+
+/*
+ * The rolling cache of gdn_window_attention_step: k_cache [B, window + sinks, Hkv,
+ * d_k] and v_cache [B, window + sinks, Hkv, d_v], bf16.  Token p of a session lies in
+ *     slot(p) = p                                    for p < sinks,
+ *               sinks + (p - sinks) mod window       otherwise,
+ * so the slots 0 .. min(window + sinks, p + 1) - 1 hold what position p sees.
+ *
+ * gdn_window_cache_append copies the tokens of k and v ([B, T, Hkv, d] through batch
+ * and row strides, a row's heads contiguous) that stay visible after the call into
+ * their slots: tokens start[b] .. start[b] + lengths[b] - 1 (start NULL: 0; lengths
+ * NULL: T).  Other slots are left as they were; a session with a negative start is
+ * passed over.  The cache's contents need no initialisation.
+ */
+int gdn_window_cache_append(const void* k, long long k_batch_stride, long long k_row_stride,
+                            const void* v, long long v_batch_stride, long long v_row_stride,
+                            void* k_cache, void* v_cache, const int* start, const int* lengths,
+                            int B, int T, int Hkv, int d_k, int d_v, int window, int sinks, cudaStream_t stream);
+
+/*
+ * One token per session: puts k [B, Hkv, d_k] and v [B, Hkv, d_v] into the caches as
+ * token pos[b] and writes out [B, Hq, d_v] = the attention of q [B, Hq, d_k] over
+ * what that position sees.  pos (device, int32 [B]) counts from 0; the session's
+ * tokens before it must be in the cache.  pos[b] < 0 marks an idle session: its
+ * cache and its row of out are left as they were.  Heads, sizes and rounding as in
+ * gdn_window_attention.
+ */
+int gdn_window_attention_step(const void* q, long long q_batch_stride, const void* k, long long k_batch_stride,
+                              const void* v, long long v_batch_stride, void* k_cache, void* v_cache,
+                              const int* pos, void* out, int B, int Hq, int Hkv, int d_k, int d_v,
+                              int window, int sinks, float scale, cudaStream_t stream);
 
 /* Human-readable text of a gdn_status value (static storage). */
 const char* gdn_status_string(int status);
