@@ -10,6 +10,7 @@
 // so the tokens visible at position p are exactly slots 0 .. min(window + sinks, p + 1) - 1,
 // in an order that the softmax does not see.
 #include "gdn_common.cuh"
+#include "gdn_sm100.cuh"
 
 namespace gdn {
 
@@ -87,25 +88,381 @@ struct Row {
     }
 };
 
-constexpr int kWarps = 8;
+// ---- whole prompts: tcgen05 ----
+//
+// One CTA per pair of 128-query tiles (two query heads that share a key head where there are
+// such, else two tiles of consecutive queries), which read the same K and V tiles:
+//   S_q = Q_q K^T on the tensor cores into TMEM, q = 0, 1;
+//   softmax of tile q by its own four warps, one thread per query row, against a lazily moved
+//     reference maximum m (it moves only when a score exceeds it by more than 2^8, so O is
+//     rarely rescaled; the division by the running sum at the end is exact for any m);
+//   P in bf16 over the score columns it came from, O_q += P_q V with P as the A operand.
+// Warp 8 issues the MMAs in the order PV_0(j-1) S_0(j) PV_1(j-1) S_1(j), so that the tensor
+// cores work for one tile while the other's softmax runs; they execute in order, so S_q(j)
+// may overwrite P_q(j-1), and "scores ready" of step j also says that PV_q(j-1) is done.
+// Warp 9 keeps K (3 stages) and V (2 stages) coming by TMA.  Key tiles are counted from the
+// window's first key, sink tiles before them when the two do not touch, so no key is visited
+// twice; a tile that a query tile sees nothing of is skipped for it.  Every wait is bounded.
+namespace tc {
 
-__global__ void __launch_bounds__(32 * kWarps)
-window_attn_kernel(const WindowArgs a)
-{
-    const int lane = threadIdx.x & 31, i = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.Hq / a.Hkv);
-    const int n = a.lengths ? min(max(a.lengths[b], 0), a.Tk) : a.Tk;
-    const int t = a.Tk - a.Tq + i;
-    if (i >= a.Tq || t >= n) return;
-    Row r;
-    r.load(a.q + b * a.q_batch + i * a.q_row + h * a.q_head, a.dk, a.scale, lane);
-    const __nv_bfloat16* k = a.k + b * a.k_batch + hk * a.k_head;
-    const __nv_bfloat16* v = a.v + b * a.v_batch + hk * a.v_head;
-    const int lo = max(0, t - a.window + 1);
-    for (int s = 0; s < min(a.sinks, lo); ++s) r.key(k + s * a.k_row, v + s * a.v_row, a.dk, a.dv, lane);
-    for (int s = lo; s <= t; ++s) r.key(k + s * a.k_row, v + s * a.v_row, a.dk, a.dv, lane);
-    r.store(a.out + (((long long)b * a.Tq + i) * a.Hq + h) * a.dv, a.dv, lane);
+using namespace sm100;
+
+constexpr int kBM = 128, kBN = 128;            // queries per tile, keys per tile
+constexpr int kSoftWarps = 8;                  // four per query tile
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kThreads = 320;
+constexpr uint32_t kBox = 128u * 128u;         // one 64-column SW128 box of 128 rows
+constexpr uint32_t kOp = 2u * kBox;            // a 128 x (d <= 128) operand
+constexpr int kKStages = 3, kVStages = 2;
+constexpr uint32_t kOffQ = 0;
+constexpr uint32_t kOffK = kOffQ + 2 * kOp;
+constexpr uint32_t kOffV = kOffK + kKStages * kOp;
+constexpr uint32_t kOffBar = kOffV + kVStages * kOp;
+enum : uint32_t { kBarQ = 0, kBarKFull = 1, kBarKFree = kBarKFull + kKStages, kBarVFull = kBarKFree + kKStages,
+                  kBarVFree = kBarVFull + kVStages, kBarS = kBarVFree + kVStages,   // [2] scores ready
+                  kBarP = kBarS + 2,           // [2] P written, O rescaled (one arrival per softmax warp)
+                  kBarO = kBarP + 2,           // [2] last PV of the tile done
+                  kBarDrain = kBarO + 2,       // every MMA done
+                  kNumBars = kBarDrain + 1 };
+constexpr uint32_t kOffAbort = kOffBar + 8u * kNumBars;
+constexpr uint32_t kOffTmemSlot = kOffAbort + 8u;
+constexpr uint32_t kSmemBytes = kOffTmemSlot + 16u + 1024u;      // + slack for 1024-byte alignment
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256;     // + 128 q each
+constexpr float kMoveRef = 8.0f;               // log2 units
+constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
+
+struct Args {
+    const int* lengths;
+    __nv_bfloat16* out;
+    int Tq, Tk, Hq, group, dk, dv, window, sinks;
+    int pair_heads;                            // the CTA's two tiles: two heads, or two tiles of one head
+    int row_blocks, head_blocks;
+    float scale_log2;
+    uint64_t wait_limit_ns;
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+    uint32_t r[32];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32"
+                 " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                   "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+
+// What a CTA visits: its two query tiles' rows and the key tiles of their union.
+struct Plan {
+    int head[2], row0[2];                      // query head and first query of tile q
+    int p_lo[2], p_hi[2];                      // positions of its first and last live query; none if p_hi < p_lo
+    int sink, startB, nA, n;                   // sink tiles 0 .. nA-1, then tiles from startB on
+    __device__ int start(int j) const { return j < nA ? kBN * j : startB + kBN * (j - nA); }
+    // does query tile q see a key of tile j?
+    __device__ bool active(int lo, int hi, int j, int window) const {
+        const int s0 = start(j);
+        return hi >= lo && s0 <= hi && (s0 < sink || s0 + kBN > lo - window + 1);
+    }
+    __device__ bool active(int q, int j, int window) const { return active(p_lo[q], p_hi[q], j, window); }
+};
+
+__device__ __forceinline__ Plan make_plan(const Args& a, int n_keys) {
+    Plan p;
+    const int off = a.Tk - a.Tq;
+    // later queries see more: their blocks come first
+    const int rb = a.row_blocks - 1 - (int)(blockIdx.x / (unsigned)a.head_blocks);
+    const int hb = (int)(blockIdx.x % (unsigned)a.head_blocks);
+    int lo = INT32_MAX, hi = -1;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        p.head[q] = a.pair_heads ? 2 * hb + q : hb;
+        p.row0[q] = a.pair_heads ? rb * kBM : (2 * rb + q) * kBM;
+        p.p_lo[q] = off + p.row0[q];
+        p.p_hi[q] = min(off + min(p.row0[q] + kBM, a.Tq), n_keys) - 1;
+        if (p.p_hi[q] >= p.p_lo[q]) {
+            lo = min(lo, p.p_lo[q]);
+            hi = max(hi, p.p_hi[q]);
+        }
+    }
+    const int w_lo = max(0, lo - a.window + 1);
+    p.sink = min(a.sinks, n_keys);
+    const bool split = w_lo > p.sink;
+    p.nA = split ? (p.sink + kBN - 1) / kBN : 0;
+    p.startB = split ? w_lo : 0;
+    p.n = hi < 0 ? 0 : p.nA + (hi + 1 - p.startB + kBN - 1) / kBN;
+    return p;
+}
+
+__device__ __forceinline__ uint64_t kmaj(uint32_t addr) { return smem_desc(addr, 16, 1024, kSwizzle128); }
+__device__ __forceinline__ uint32_t kstep(uint32_t op, int ks) {
+    return op + (ks >= 4 ? kBox : 0u) + (uint32_t)(ks & 3) * 32u;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const Args a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* gb = smem_raw + (base - raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int b = blockIdx.y;
+    const int n_keys = a.lengths ? min(max(a.lengths[b], 0), a.Tk) : a.Tk;
+    const Plan p = make_plan(a, n_keys);
+    if (p.n == 0) return;                      // all padding
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(gb + kOffAbort);
+    auto bar = [&](uint32_t i) { return base + kOffBar + 8u * i; };
+    const uint64_t lim = a.wait_limit_ns;
+    const int nbk = (a.dk + 63) / 64, nbv = (a.dv + 63) / 64;       // 64-column boxes per operand
+
+    if (warp == 0) {
+        tmem_alloc(base + kOffTmemSlot, kTmemCols);
+        tmem_relinquish();
+    }
+    if (tid == 32) {
+        for (uint32_t i = 0; i < kNumBars; ++i) mbar_init(bar(i), (i >= kBarP && i < kBarP + 2) ? 4u : 1u);
+        fence_mbar_init();
+        *abort_flag = 0;
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gb + kOffTmemSlot);
+
+    if (warp == kLoadWarp) {
+        // ======================= copies =======================
+        const int hk = p.head[0] / a.group;
+        bool ok = true;
+        int k_issued = 0, v_issued = 0;
+        if (lane == 0) {
+            const uint32_t live = (p.p_hi[0] >= p.p_lo[0] ? 1u : 0u) + (p.p_hi[1] >= p.p_lo[1] ? 1u : 0u);
+            mbar_arrive_expect_tx(bar(kBarQ), live * (uint32_t)nbk * kBox);
+            for (int q = 0; q < 2; ++q)
+                if (p.p_hi[q] >= p.p_lo[q])
+                    for (int c = 0; c < nbk; ++c)
+                        tma_load_4d(base + kOffQ + q * kOp + c * kBox, &tm_q, bar(kBarQ), 64 * c, p.head[q], p.row0[q], b);
+            for (int j = 0; ok && j < p.n; ++j) {
+                const int sk = j % kKStages, sv = j % kVStages;
+                if (j >= kKStages)
+                    ok = mbar_wait(bar(kBarKFree + sk), (uint32_t)((j / kKStages - 1) & 1), abort_flag, lim, 41);
+                if (!ok) break;
+                mbar_arrive_expect_tx(bar(kBarKFull + sk), (uint32_t)nbk * kBox);
+                for (int c = 0; c < nbk; ++c)
+                    tma_load_4d(base + kOffK + sk * kOp + c * kBox, &tm_k, bar(kBarKFull + sk), 64 * c, hk, p.start(j), b);
+                k_issued = j + 1;
+                if (j >= kVStages)
+                    ok = mbar_wait(bar(kBarVFree + sv), (uint32_t)((j / kVStages - 1) & 1), abort_flag, lim, 42);
+                if (!ok) break;
+                mbar_arrive_expect_tx(bar(kBarVFull + sv), (uint32_t)nbv * kBox);
+                for (int c = 0; c < nbv; ++c)
+                    tma_load_4d(base + kOffV + sv * kOp + c * kBox, &tm_v, bar(kBarVFull + sv), 64 * c, hk, p.start(j), b);
+                v_issued = j + 1;
+            }
+            // copies land before shared memory goes away, whoever gave up: the last one of each stage is
+            // enough (a stage is refilled only after its tile was read)
+            drain_wait(bar(kBarQ), 0);
+            for (int j = max(0, k_issued - kKStages); j < k_issued; ++j)
+                drain_wait(bar(kBarKFull + j % kKStages), (uint32_t)((j / kKStages) & 1));
+            for (int j = max(0, v_issued - kVStages); j < v_issued; ++j)
+                drain_wait(bar(kBarVFull + j % kVStages), (uint32_t)((j / kVStages) & 1));
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ======================= MMAs =======================
+        const int nks = a.dk / 16;
+        const uint32_t idpv = idesc_bf16(128, a.dv, false, true);
+        bool ok = true;
+        auto wait = [&](uint32_t i, uint32_t parity, int code) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(i), parity & 1u, abort_flag, lim, code));
+            return ok;
+        };
+        int steps[2] = {0, 0};                 // key tiles whose P V was issued
+        wait(kBarQ, 0, 43);
+        for (int j = 0; ok && j <= p.n; ++j) {
+            const bool last_v = j >= 1 && p.active(1, j - 1, a.window);      // tile 1 is V's last reader
+            const bool last_k = j < p.n && p.active(1, j, a.window);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (j >= 1 && p.active(q, j - 1, a.window)) {
+                    const int sv = (j - 1) % kVStages;
+                    const uint32_t v = base + kOffV + sv * kOp;
+                    if (!wait(kBarVFull + sv, (uint32_t)((j - 1) / kVStages), 44)) break;
+                    // rows of padding in V hold anything: zero times that must be zero
+                    const int live = n_keys - p.start(j - 1);
+                    if (live < kBN && n_keys < a.Tk && (q == 0 || !p.active(0, j - 1, a.window))) {
+                        for (int r = live * 8 + lane; r < kBN * 8; r += 32)
+                            for (int c = 0; c < nbv; ++c) st_shared_v4(v + c * kBox + 16u * r, 0, 0, 0, 0);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (!wait(kBarP + q, (uint32_t)steps[q], 45)) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < kBN / 16; ++ks)
+                        attn::mma_bf16_tmem_a_warp(tmem + kColO + 128u * q, tmem + kColS + 128u * q + 8u * ks,
+                                                   smem_desc(v + (uint32_t)ks * 2048u, kBox, 1024, kSwizzle128), idpv,
+                                                   (steps[q] > 0 || ks > 0) ? 1u : 0u);
+                    ++steps[q];
+                    if (q == 1 || !last_v) mma_commit_warp(bar(kBarVFree + sv));
+                    bool more = false;
+                    for (int jj = j; jj < p.n && !more; ++jj) more = p.active(q, jj, a.window);
+                    if (!more) mma_commit_warp(bar(kBarO + q));
+                }
+                if (j < p.n && p.active(q, j, a.window)) {
+                    const int sk = j % kKStages;
+                    if (!wait(kBarKFull + sk, (uint32_t)(j / kKStages), 46)) break;
+                    tc_fence_after();
+                    const uint32_t qo = base + kOffQ + q * kOp, ko = base + kOffK + sk * kOp;
+#pragma unroll 1
+                    for (int ks = 0; ks < nks; ++ks)
+                        mma_bf16_warp(tmem + kColS + 128u * q, kmaj(kstep(qo, ks)), kmaj(kstep(ko, ks)), kIdS, ks > 0);
+                    mma_commit_warp(bar(kBarS + q));
+                    if (q == 1 || !last_k) mma_commit_warp(bar(kBarKFree + sk));
+                }
+            }
+        }
+        // every MMA is done before shared memory and TMEM go away, whoever gave up
+        mma_commit_warp(bar(kBarDrain));
+        if (lane == 0) drain_wait(bar(kBarDrain), 0);
+        __syncwarp();
+    } else {
+        // ======================= softmax of tile q, one thread per row =======================
+        const int q = warp >> 2;
+        const int p_lo = q ? p.p_lo[1] : p.p_lo[0], p_hi = q ? p.p_hi[1] : p.p_hi[0];
+        const int row0 = q ? p.row0[1] : p.row0[0], head = q ? p.head[1] : p.head[0];
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t ts = lane_base + kColS + 128u * q, to = lane_base + kColO + 128u * q;
+        const int row = (warp & 3) * 32 + lane;
+        const int t = p_lo + row;                             // this row's position
+        const int ws = max(0, t - a.window + 1);
+        const bool split = p.startB > 0 || p.nA > 0;
+        float m_ref = -INFINITY, l = 0.0f;
+        bool ok = true;
+        int i = 0;                                            // key tiles taken
+        for (int j = 0; j < p.n; ++j) {
+            if (!p.active(p_lo, p_hi, j, a.window)) continue;
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarS + q), (uint32_t)(i & 1), abort_flag, lim, 47));
+            if (!ok) break;
+            tc_fence_after();
+            float x[kBN];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32u * c, x + 32 * c);
+            const int s0 = p.start(j);
+            const bool sink_tile = j < p.nA;
+            // columns [lo, hi] are in the row's window, columns below sk among the sinks
+            const int hi = sink_tile ? -1 : min(t, n_keys - 1) - s0;
+            const int lo = ws - s0, sk = (split && !sink_tile) ? 0 : min(p.sink, t + 1) - s0;
+            const bool full = (lo <= 0 && hi >= kBN - 1) || sk >= kBN;
+            tmem_wait_ld();
+            if (__any_sync(0xffffffffu, !full)) {
+#pragma unroll
+                for (int e = 0; e < kBN; ++e) x[e] = ((e >= lo && e <= hi) || e < sk) ? x[e] : -INFINITY;
+            }
+            float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+            for (int e = 0; e < (kBN - 4) / 2; ++e) mx[e & 3] = attn::max3f(mx[e & 3], x[4 + 2 * e], x[5 + 2 * e]);
+            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+            const bool move = mt > m_ref + kMoveRef;
+            float alpha = 1.0f;
+            if (move) {
+                alpha = attn::ex2(m_ref - mt);
+                m_ref = mt;
+            }
+            // O is rescaled where a row of the warp moved (TMEM accesses are warp-collective); its
+            // last P V is done, since the scores that followed it are here
+            if (i > 0 && __any_sync(0xffffffffu, move)) {
+#pragma unroll 1
+                for (int c = 0; c < a.dv / 16; ++c) {
+                    float o[16];
+                    tmem_ld16(to + 16u * c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] *= alpha;
+                    attn::tmem_st16(to + 16u * c, o);
+                }
+            }
+            const float neg_mr = (m_ref == -INFINITY) ? 0.0f : -m_ref;
+            const uint64_t sc2 = attn::f2pack(a.scale_log2, a.scale_log2), nm2 = attn::f2pack(neg_mr, neg_mr);
+            uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float t0, t1;
+                    attn::f2unpack(attn::fma2(attn::f2pack(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]), sc2, nm2), t0, t1);
+                    const float p0 = attn::ex2(t0), p1 = attn::ex2(t1);
+                    acc[e & 3] = attn::add2(acc[e & 3], attn::f2pack(p0, p1));
+                    pk[e] = pack_bf16x2(p0, p1);
+                }
+                attn::tmem_st16u(ts + 16u * c, pk);
+            }
+            float sm[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) attn::f2unpack(acc[e], sm[2 * e], sm[2 * e + 1]);
+            l = l * alpha + (((sm[0] + sm[1]) + (sm[2] + sm[3])) + ((sm[4] + sm[5]) + (sm[6] + sm[7])));
+            attn::tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarP + q));
+            ++i;
+        }
+        if (ok && i > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarO + q), 0, abort_flag, lim, 48));
+            if (ok) {
+                tc_fence_after();
+                const float inv = 1.0f / l;
+                __nv_bfloat16* orow = a.out + (((long long)b * a.Tq + row0 + row) * a.Hq + head) * a.dv;
+#pragma unroll 1
+                for (int c = 0; c < a.dv / 16; ++c) {
+                    float o[16];
+                    tmem_ld16(to + 16u * c, o);
+                    tmem_wait_ld();
+                    if (t <= p_hi) {
+                        uint4* dst = reinterpret_cast<uint4*>(orow + 16 * c);
+                        dst[0] = make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
+                                            pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
+                        dst[1] = make_uint4(pack_bf16x2(o[8] * inv, o[9] * inv), pack_bf16x2(o[10] * inv, o[11] * inv),
+                                            pack_bf16x2(o[12] * inv, o[13] * inv), pack_bf16x2(o[14] * inv, o[15] * inv));
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// 4-D bf16 map over a strided [B, T, H, d] tensor, box {64, 1, 128, 1}, 128-byte swizzle.
+bool make_map(CUtensorMap* map, const void* ptr, int d, int H, int T, int B, long long head, long long row,
+              long long batch)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
+    cuuint64_t strides[3] = {(cuuint64_t)head * 2, (cuuint64_t)row * 2, (cuuint64_t)batch * 2};
+    cuuint32_t box[4] = {64, 1, kBN, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace tc
 
 // One warp per query head and session.
 __global__ void __launch_bounds__(32)
@@ -168,8 +525,29 @@ window_append_kernel(const AppendArgs a)
 
 cudaError_t launch_window(const WindowArgs& a, cudaStream_t stream)
 {
-    const dim3 grid((unsigned)((a.Tq + window::kWarps - 1) / window::kWarps), (unsigned)a.Hq, (unsigned)a.B);
-    window::window_attn_kernel<<<grid, 32 * window::kWarps, 0, stream>>>(a);
+    using namespace window::tc;
+    CUtensorMap mq, mk, mv;
+    if (!make_map(&mq, a.q, a.dk, a.Hq, a.Tq, a.B, a.q_head, a.q_row, a.q_batch) ||
+        !make_map(&mk, a.k, a.dk, a.Hkv, a.Tk, a.B, a.k_head, a.k_row, a.k_batch) ||
+        !make_map(&mv, a.v, a.dv, a.Hkv, a.Tk, a.B, a.v_head, a.v_row, a.v_batch))
+        return cudaErrorInvalidValue;
+    // (a per-device setting of the current context: set on every call)
+    cudaError_t e = cudaFuncSetAttribute(window_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    if (e != cudaSuccess) return e;
+    Args r;
+    r.lengths = a.lengths;
+    r.out = a.out;
+    r.Tq = a.Tq; r.Tk = a.Tk; r.Hq = a.Hq; r.group = a.Hq / a.Hkv; r.dk = a.dk; r.dv = a.dv;
+    r.window = a.window; r.sinks = a.sinks;
+    r.pair_heads = r.group % 2 == 0;
+    const int tiles = (a.Tq + kBM - 1) / kBM;
+    r.row_blocks = r.pair_heads ? tiles : (tiles + 1) / 2;
+    r.head_blocks = r.pair_heads ? a.Hq / 2 : a.Hq;
+    r.scale_log2 = 1.4426950408889634f * a.scale;
+    r.wait_limit_ns = g_wait_limit_ns;
+    const long long blocks = (long long)r.row_blocks * r.head_blocks;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    window_attn_kernel<<<dim3((unsigned)blocks, (unsigned)a.B), kThreads, kSmemBytes, stream>>>(mq, mk, mv, r);
     return cudaGetLastError();
 }
 

@@ -510,6 +510,23 @@ def test_captured_and_replayed_beside_eager_calls(cuda):
         assert torch.equal(kc, kv[0]) and torch.equal(vc, kv[1])
 
 
+def test_window_attention_timeout_is_reported_and_recovers(cuda):
+    """A wait that runs out (the bound shortened to 1 ns) is reported, and the next call is right."""
+    g = gen(12)
+    q, k, v = attn_inputs(g, 1, 2000, 2000, 4, 2, 112, 112)
+    want = G.window_attention(q, k, v, 500, 20)
+    done()
+    try:
+        G.gdn_set_wait_limit_ns(1)
+        G.window_attention(q, k, v, 500, 20)
+        assert G.gdn_get_last_device_status() == G.GDN_ERR_TIMEOUT
+    finally:
+        G.gdn_set_wait_limit_ns(0)
+    got = G.window_attention(q, k, v, 500, 20)
+    done()
+    assert torch.equal(got, want)
+
+
 def test_python_calls_check_shapes_and_types(cuda):
     t = torch.bfloat16
     x, w = torch.zeros(2, 4, 16, dtype=t, device=cuda), torch.zeros(16, 4, device=cuda)
