@@ -11,6 +11,7 @@
 // kBatch rows are issued before the first is used.  Channels are the fastest thread index,
 // so a warp reads and writes 512 contiguous bytes of a row.
 #include "gdn_common.cuh"
+#include "gdn_sm100.cuh"
 
 namespace gdn {
 
@@ -33,13 +34,34 @@ constexpr int kStretch = 16;   // tokens per thread; a stretch is longer than th
                                // stretch 0 reads state_in and state_out may be the same memory
 constexpr int kBatch = 8;
 
-template <typename IOT> struct Vec {
-    static constexpr int n = 16 / sizeof(IOT);
-    union { uint4 raw; IOT e[n]; };
-    __device__ Vec() {}
+// A 16-byte vector of channels as pairs of f32 in 64-bit registers, the form of the paired FMA.
+template <typename IOT> struct Vec;
+template <> struct Vec<__nv_bfloat16> {
+    static constexpr int n = 8;
+    __device__ static uint64_t pair(const uint4& v, int i) {
+        const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+        return attn::f2pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    __device__ static uint4 pack(const float (&f)[8]) {
+        return make_uint4(sm100::pack_bf16x2(f[0], f[1]), sm100::pack_bf16x2(f[2], f[3]),
+                          sm100::pack_bf16x2(f[4], f[5]), sm100::pack_bf16x2(f[6], f[7]));
+    }
+};
+template <> struct Vec<float> {
+    static constexpr int n = 4;
+    __device__ static uint64_t pair(const uint4& v, int i) {
+        return i == 0 ? attn::f2pack(__uint_as_float(v.x), __uint_as_float(v.y))
+                      : attn::f2pack(__uint_as_float(v.z), __uint_as_float(v.w));
+    }
+    __device__ static uint4 pack(const float (&f)[4]) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
 };
 
-__device__ __forceinline__ float silu_f(float y) { return y / (1.0f + __expf(-y)); }
+// y / (1 + e^-y); the quotient far below 0 is 0
+__device__ __forceinline__ float silu_f(float y) {
+    return __fdividef(y, 1.0f + attn::ex2(-1.4426950408889634f * y));
+}
 
 template <typename IOT, int W, bool SILU>
 __global__ void __launch_bounds__(kThreads)
@@ -59,61 +81,64 @@ causal_conv_kernel(const ConvArgs a)
 
     // the row of token t; tokens before the call come from the carried state
     auto row = [&](int t) {
-        Vec<IOT> v;
-        if (t >= 0) v.raw = *reinterpret_cast<const uint4*>(x + t * a.x_row);
-        else if (st) v.raw = *reinterpret_cast<const uint4*>(st + (long long)(t + W - 1) * a.D);
-        else v.raw = make_uint4(0, 0, 0, 0);
-        return v;
+        if (t >= 0) return __ldg(reinterpret_cast<const uint4*>(x + t * a.x_row));
+        if (st) return *reinterpret_cast<const uint4*>(st + (long long)(t + W - 1) * a.D);
+        return make_uint4(0, 0, 0, 0);
     };
 
     if (t0 < t1) {
-        float w[V][W], bias[V], win[W - 1][V];
+        uint64_t w[W][V / 2], bias[V / 2], win[W - 1][V / 2];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            bias[e] = a.bias ? __ldg(a.bias + c + e) : 0.0f;
+        for (int e = 0; e < V / 2; ++e) {
+            bias[e] = a.bias ? attn::f2pack(__ldg(a.bias + c + 2 * e), __ldg(a.bias + c + 2 * e + 1)) : 0ull;
 #pragma unroll
-            for (int j = 0; j < W; ++j) w[e][j] = __ldg(a.weight + (long long)(c + e) * W + j);
+            for (int j = 0; j < W; ++j)
+                w[j][e] = attn::f2pack(__ldg(a.weight + (long long)(c + 2 * e) * W + j),
+                                       __ldg(a.weight + (long long)(c + 2 * e + 1) * W + j));
         }
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
-            const Vec<IOT> v = row(t0 - (W - 1) + j);
+            const uint4 v = row(t0 - (W - 1) + j);
 #pragma unroll
-            for (int e = 0; e < V; ++e) win[j][e] = to_f32(v.e[e]);
+            for (int e = 0; e < V / 2; ++e) win[j][e] = Vec<IOT>::pair(v, e);
         }
         IOT* o = static_cast<IOT*>(a.out) + ((long long)b * a.T + t0) * a.D + c;
+#pragma unroll 1
         for (int t = t0; t < t1; t += kBatch) {
-            Vec<IOT> in[kBatch];
+            uint4 in[kBatch];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (t + i < t1) in[i] = row(t + i);
+            for (int i = 0; i < kBatch; ++i) in[i] = row(min(t + i, t1 - 1));
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                if (t + i >= t1) break;
-                Vec<IOT> r;
+                float r[V];
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float xe = to_f32(in[i].e[e]);
-                    float y = bias[e];
+                for (int e = 0; e < V / 2; ++e) {
+                    const uint64_t xe = Vec<IOT>::pair(in[i], e);
+                    uint64_t y = bias[e];
 #pragma unroll
-                    for (int j = 0; j < W - 1; ++j) y = fmaf(w[e][j], win[j][e], y);
-                    y = fmaf(w[e][W - 1], xe, y);
+                    for (int j = 0; j < W - 1; ++j) y = attn::fma2(w[j][e], win[j][e], y);
+                    y = attn::fma2(w[W - 1][e], xe, y);
 #pragma unroll
                     for (int j = 0; j + 1 < W - 1; ++j) win[j][e] = win[j + 1][e];
                     win[W - 2][e] = xe;
-                    r.e[e] = from_f32<IOT>(SILU ? silu_f(y) : y);
+                    attn::f2unpack(y, r[2 * e], r[2 * e + 1]);
+                    if (SILU) {
+                        r[2 * e] = silu_f(r[2 * e]);
+                        r[2 * e + 1] = silu_f(r[2 * e + 1]);
+                    }
                 }
-                *reinterpret_cast<uint4*>(o) = r.raw;
+                if (t + i < t1) *reinterpret_cast<uint4*>(o) = Vec<IOT>::pack(r);
                 o += a.D;
             }
         }
     }
     if (s == 0 && a.state_out) {
-        Vec<IOT> keep[W - 1];
+        uint4 keep[W - 1];
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) keep[j] = row(n - (W - 1) + j);     // read before the state is written
         IOT* so = static_cast<IOT*>(a.state_out) + (long long)b * (W - 1) * a.D + c;
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) *reinterpret_cast<uint4*>(so + (long long)j * a.D) = keep[j].raw;
+        for (int j = 0; j < W - 1; ++j) *reinterpret_cast<uint4*>(so + (long long)j * a.D) = keep[j];
     }
 }
 

@@ -66,7 +66,7 @@ int run_conv(gdn::ConvArgs a, int width, int silu, size_t elem, cudaStream_t str
                                : gdn::launch_conv<float>(a, width, silu != 0, stream));
 }
 
-int run_scan(gdn::ScanArgs a, int softplus, size_t elem, cudaStream_t stream)
+int run_scan(gdn::ScanArgs a, int softplus, size_t elem, bool step, cudaStream_t stream)
 {
     if (a.B < 1 || a.T < 0 || a.D < 1 || a.N < 1 || (softplus != 0 && softplus != 1)) return GDN_ERR_INVALID_ARG;
     if ((a.N != 8 && a.N != 16 && a.N != 32 && a.N != 64) || a.D % 8 || a.B > 65535) return GDN_ERR_UNSUPPORTED;
@@ -95,7 +95,8 @@ int run_scan(gdn::ScanArgs a, int softplus, size_t elem, cudaStream_t stream)
     if (a.state_out && (overlaps_any(a.state_out, ns, in) ||
                         (a.state_out != a.state_in && overlaps(a.state_out, ns, a.state_in, ns))))
         return GDN_ERR_INVALID_ARG;
-    return to_status(elem == 2 ? gdn::launch_scan<__nv_bfloat16>(a, stream) : gdn::launch_scan<float>(a, stream));
+    return to_status(elem == 2 ? gdn::launch_scan<__nv_bfloat16>(a, step, stream)
+                               : gdn::launch_scan<float>(a, step, stream));
 }
 
 bool head_dim_ok(int d) { return d >= 16 && d <= 128 && d % 16 == 0; }
@@ -172,7 +173,7 @@ int gdn_selective_scan(const void* x, long long x_batch_stride, long long x_row_
 {
     return run_scan({x, dt, z, Bm, Cm, x_batch_stride, x_row_stride, dt_batch_stride, dt_row_stride, z_batch_stride,
                      z_row_stride, b_batch_stride, b_row_stride, c_batch_stride, c_row_stride, A, skip, dt_bias,
-                     state_in, state_out, lengths, y, B, T, D, N, false}, dt_softplus, 2, stream);
+                     state_in, state_out, lengths, y, B, T, D, N, false}, dt_softplus, 2, false, stream);
 }
 
 int gdn_selective_scan_f32(const float* x, long long x_batch_stride, long long x_row_stride,
@@ -186,7 +187,7 @@ int gdn_selective_scan_f32(const float* x, long long x_batch_stride, long long x
 {
     return run_scan({x, dt, z, Bm, Cm, x_batch_stride, x_row_stride, dt_batch_stride, dt_row_stride, z_batch_stride,
                      z_row_stride, b_batch_stride, b_row_stride, c_batch_stride, c_row_stride, A, skip, dt_bias,
-                     state_in, state_out, lengths, y, B, T, D, N, false}, dt_softplus, 4, stream);
+                     state_in, state_out, lengths, y, B, T, D, N, false}, dt_softplus, 4, false, stream);
 }
 
 int gdn_selective_scan_step(const void* x, long long x_batch_stride, const void* dt, long long dt_batch_stride,
@@ -198,7 +199,7 @@ int gdn_selective_scan_step(const void* x, long long x_batch_stride, const void*
     if (!state) return GDN_ERR_INVALID_ARG;
     return run_scan({x, dt, z, Bm, Cm, x_batch_stride, D, dt_batch_stride, D, z_batch_stride, D, b_batch_stride, N,
                      c_batch_stride, N, A, skip, dt_bias, state, state, nullptr, y, B, 1, D, N, false},
-                    dt_softplus, 2, stream);
+                    dt_softplus, 2, true, stream);
 }
 
 int gdn_selective_scan_step_f32(const float* x, long long x_batch_stride, const float* dt, long long dt_batch_stride,
@@ -210,7 +211,7 @@ int gdn_selective_scan_step_f32(const float* x, long long x_batch_stride, const 
     if (!state) return GDN_ERR_INVALID_ARG;
     return run_scan({x, dt, z, Bm, Cm, x_batch_stride, D, dt_batch_stride, D, z_batch_stride, D, b_batch_stride, N,
                      c_batch_stride, N, A, skip, dt_bias, state, state, nullptr, y, B, 1, D, N, false},
-                    dt_softplus, 4, stream);
+                    dt_softplus, 4, true, stream);
 }
 
 int gdn_window_attention(const void* q, long long q_batch_stride, long long q_row_stride, long long q_head_stride,
