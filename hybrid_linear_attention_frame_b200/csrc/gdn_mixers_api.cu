@@ -257,7 +257,7 @@ int gdn_window_cache_append(const void* k, long long k_batch_stride, long long k
     int st = check_window(B, Hkv, Hkv, d_k, d_v, window, sinks, 1.0f);
     if (st != GDN_OK) return st;
     if (T < 0) return GDN_ERR_INVALID_ARG;
-    if ((int64_t)window + sinks > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+    if ((int64_t)window + sinks > INT32_MAX - 64) return GDN_ERR_UNSUPPORTED;
     if (T == 0) return GDN_OK;
     if (!k || !v || !k_cache || !v_cache || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(start, 4) ||
         !aligned(lengths, 4))
@@ -290,7 +290,7 @@ int gdn_window_attention_step(const void* q, long long q_batch_stride, const voi
 {
     int st = check_window(B, Hq, Hkv, d_k, d_v, window, sinks, scale);
     if (st != GDN_OK) return st;
-    if ((int64_t)window + sinks > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+    if ((int64_t)window + sinks > INT32_MAX - 64) return GDN_ERR_UNSUPPORTED;
     if (!q || !k || !v || !k_cache || !v_cache || !pos || !out) return GDN_ERR_INVALID_ARG;
     if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) || !aligned(pos, 4))
         return GDN_ERR_INVALID_ARG;

@@ -48,46 +48,6 @@ __host__ __device__ __forceinline__ long long cache_slot(long long p, int window
     return p < sinks ? p : sinks + (p - sinks) % window;
 }
 
-// One warp's softmax state for one query: lane i holds the head's elements 2 i, 2 i + 1, 64 + 2 i, 65 + 2 i.
-struct Row {
-    float q[4], acc[4], m, l;
-    __device__ void load(const __nv_bfloat16* p, int d, float scale, int lane) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = 64 * (i >> 1) + 2 * lane + (i & 1);
-            q[i] = e < d ? __bfloat162float(p[e]) * scale : 0.0f;
-            acc[i] = 0.0f;
-        }
-        m = -INFINITY;
-        l = 0.0f;
-    }
-    __device__ void key(const __nv_bfloat16* k, const __nv_bfloat16* v, int dk, int dv, int lane) {
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = 64 * (i >> 1) + 2 * lane + (i & 1);
-            if (e < dk) s = fmaf(q[i], __bfloat162float(k[e]), s);
-        }
-#pragma unroll
-        for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
-        const float mn = fmaxf(m, s), f = __expf(m - mn), p = __expf(s - mn);
-        l = l * f + p;
-        m = mn;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = 64 * (i >> 1) + 2 * lane + (i & 1);
-            acc[i] = acc[i] * f + (e < dv ? p * __bfloat162float(v[e]) : 0.0f);
-        }
-    }
-    __device__ void store(__nv_bfloat16* o, int dv, int lane) const {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = 64 * (i >> 1) + 2 * lane + (i & 1);
-            if (e < dv) o[e] = __float2bfloat16_rn(acc[i] / l);
-        }
-    }
-};
-
 // ---- whole prompts: tcgen05 ----
 //
 // One CTA per pair of 128-query tiles (two query heads that share a key head where there are
@@ -464,33 +424,308 @@ bool make_map(CUtensorMap* map, const void* ptr, int d, int H, int T, int B, lon
 
 }  // namespace tc
 
-// One warp per query head and session.
-__global__ void __launch_bounds__(32)
+// ---- one token per session ----
+//
+// The cache is read once for all query heads of a key head, so HBM bounds it.  Sixteen query
+// heads are the rows of mma.sync m16n8k16 tiles (tcgen05 takes 64 rows at least, of which a
+// group fills a few): with 16 slots a tile, a warp's scores, softmax and P V stay in its
+// registers, and a warp needs no other one until the end.  Each warp streams its tiles
+// (every warp of the cluster takes its turn) through a private ring of cp.async stages, so
+// kStages - 1 tiles per warp are in flight and no barrier stands in the loop.  The cluster's CTAs
+// split one session and key head; the warps' partial sums (maximum, sum, O) meet in shared
+// memory, the CTAs' through distributed shared memory in a fixed order: one launch, no
+// workspace, the same bits every time.  P enters as a bf16 pair (value and remainder), since
+// the tensor cores have time to spare here: the result is rounded once, like a plain form's.
+namespace step {
+
+using namespace sm100;
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kRows = 16, kSlots = 16;         // query heads, cache slots per tile
+constexpr int kStages = 4;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
+    const int n = on ? 16 : 0;                 // 0 bytes read: the destination is filled with zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t cluster_rank() { uint32_t r; asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r)); return r; }
+__device__ __forceinline__ uint32_t cluster_size() { uint32_t r; asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r)); return r; }
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_remote(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
+    return v;
+}
+
+// Bytes of one stage (16 rows of K and of V; a row is padded by 16 bytes, so that the 8 rows of an
+// ldmatrix fall on different banks: d / 8 is even) and of the whole CTA.
+__host__ __device__ constexpr uint32_t row_bytes(int d) { return 2u * d + 16u; }
+__host__ __device__ constexpr uint32_t stage_bytes(int dk, int dv) { return kSlots * (row_bytes(dk) + row_bytes(dv)); }
+__host__ __device__ constexpr uint32_t part_floats(int dv) { return kRows * (dv + 2); }   // m, l and O of 16 rows
+__host__ __device__ constexpr uint32_t smem_bytes(int dk, int dv) {
+    const uint32_t ring = kWarps * kStages * stage_bytes(dk, dv), parts = (kWarps + 1) * part_floats(dv) * 4;
+    return (ring > parts ? ring : parts);
+}
+
+// DK16, DV16: the head sizes in units of 16, rounded up to what is instantiated (loops end at the
+// real ones).
+template <int DK16, int DV16>
+__global__ void __launch_bounds__(kThreads)
 window_step_kernel(const StepArgs a)
 {
-    const int lane = threadIdx.x, h = blockIdx.x, b = blockIdx.y, G = a.Hq / a.Hkv, hk = h / G;
-    const long long p = a.pos[b];
-    if (p < 0) return;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int X = (int)cluster_size(), rank = (int)cluster_rank();
+    const int G = a.Hq / a.Hkv, parts = (G + kRows - 1) / kRows;
+    const int unit = blockIdx.x / X, hk = unit / parts, g0 = (unit % parts) * kRows, b = blockIdx.y;
+    const long long pos = a.pos[b];
+    if (pos < 0) return;                       // idle: the whole cluster leaves
     const int cap = a.window + a.sinks;
-    const long long slot = cache_slot(p, a.window, a.sinks);
+    const int slot = (int)cache_slot(pos, a.window, a.sinks);
+    const int seen = pos + 1 < cap ? (int)(pos + 1) : cap;
+    const int rows = min(kRows, G - g0);
+    const int nk = a.dk / 16, nv = a.dv / 16;
     const __nv_bfloat16* kn = a.k + b * a.k_batch + hk * a.dk;
     const __nv_bfloat16* vn = a.v + b * a.v_batch + hk * a.dv;
     __nv_bfloat16* kc = a.k_cache + ((long long)b * cap * a.Hkv + hk) * a.dk;
     __nv_bfloat16* vc = a.v_cache + ((long long)b * cap * a.Hkv + hk) * a.dv;
     const long long kr = (long long)a.Hkv * a.dk, vr = (long long)a.Hkv * a.dv;
-    Row r;
-    r.load(a.q + b * a.q_batch + (long long)h * a.dk, a.dk, a.scale, lane);
-    const long long seen = p + 1 < cap ? p + 1 : cap;
-    for (long long s = 0; s < seen; ++s) {
-        const bool own = s == slot;                    // the slot is being written: read the new row itself
-        r.key(own ? kn : kc + s * kr, own ? vn : vc + s * vr, a.dk, a.dv, lane);
+
+    // Q as A fragments: row r = lane / 4 (and + 8), columns 2 (lane % 4) (and + 8) of each 16
+    uint32_t qa[DK16][4];
+    {
+        const __nv_bfloat16* q = a.q + b * a.q_batch + (long long)(hk * G + g0) * a.dk;
+        const int r = lane >> 2, c = 2 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < DK16; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int rr = r + 8 * (e & 1), cc = 16 * i + c + 8 * (e >> 1);
+                qa[i][e] = (rr < rows && i < nk) ? *reinterpret_cast<const uint32_t*>(q + (long long)rr * a.dk + cc) : 0u;
+            }
     }
-    if (h == hk * G) {
-        for (int e = lane; e < a.dk; e += 32) kc[slot * kr + e] = kn[e];
-        for (int e = lane; e < a.dv; e += 32) vc[slot * vr + e] = vn[e];
+
+    const uint32_t sb = stage_bytes(a.dk, a.dv), krb = row_bytes(a.dk), vrb = row_bytes(a.dv);
+    const uint32_t ring = smem_u32(smem) + warp * kStages * sb;
+    const int tiles = (seen + kSlots - 1) / kSlots, stride = X * kWarps, first = rank * kWarps + warp;
+    // slots past the last one seen are filled with zeros, not read; the new token's rows come from k and v
+    auto fetch = [&](int tile, int stage) {
+        const uint32_t kd = ring + stage * sb, vd = kd + kSlots * krb;
+        if (tile < tiles) {
+            const int ck = a.dk / 8, cv = a.dv / 8;
+            for (int i = lane; i < kSlots * ck; i += 32) {
+                const int r = i / ck, c = i - r * ck, s = tile * kSlots + r;
+                const __nv_bfloat16* src = s == slot ? kn : kc + (s < seen ? s : 0) * kr;
+                cp_async16(kd + r * krb + 16 * c, src + 8 * c, s < seen);
+            }
+            for (int i = lane; i < kSlots * cv; i += 32) {
+                const int r = i / cv, c = i - r * cv, s = tile * kSlots + r;
+                const __nv_bfloat16* src = s == slot ? vn : vc + (s < seen ? s : 0) * vr;
+                cp_async16(vd + r * vrb + 16 * c, src + 8 * c, s < seen);
+            }
+        }
+        cp_commit();
+    };
+
+    float o[2 * DV16][4];
+#pragma unroll
+    for (int i = 0; i < 2 * DV16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};     // rows lane / 4 and + 8; l: this thread's columns
+    const float sc = a.scale * 1.4426950408889634f;
+
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(first + i * stride, i);
+    int st = 0;
+    for (int tile = first; tile < tiles; tile += stride) {
+        cp_wait<kStages - 2>();
+        __syncwarp();
+        fetch(tile + (kStages - 1) * stride, st == 0 ? kStages - 1 : st - 1);
+        const uint32_t kd = ring + st * sb, vd = kd + kSlots * krb;
+        st = st + 1 == kStages ? 0 : st + 1;
+        // S [16 x 16] = Q K^T: K rows are the columns of B; a x4 load brings slots 0-7 and 8-15, both halves of 16 d
+        float s[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        const uint32_t ka = kd + ((lane & 7) + 8 * (lane >> 4)) * krb + 16 * ((lane >> 3) & 1);
+#pragma unroll
+        for (int i = 0; i < DK16; ++i)
+            if (i < nk) {
+                uint32_t f[4];
+                ldsm4(f, ka + 32 * i);
+                mma16816(s[0], qa[i], f[0], f[1]);
+                mma16816(s[1], qa[i], f[2], f[3]);
+            }
+        // online softmax of this warp's slots; columns 2 (lane % 4) + {0, 1} of each 8
+        const int left = seen - tile * kSlots;
+        float mt[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int col = 8 * h + 2 * (lane & 3) + (e & 1);
+                s[h][e] = col < left ? s[h][e] * sc : -INFINITY;
+                mt[e >> 1] = fmaxf(mt[e >> 1], s[h][e]);
+            }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            mt[r] = fmaxf(mt[r], __shfl_xor_sync(0xffffffffu, mt[r], 1));
+            mt[r] = fmaxf(mt[r], __shfl_xor_sync(0xffffffffu, mt[r], 2));
+        }
+        const float mn[2] = {fmaxf(m[0], mt[0]), fmaxf(m[1], mt[1])};      // finite: a tile has a slot
+        if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
+            const float f[2] = {attn::ex2(m[0] - mn[0]), attn::ex2(m[1] - mn[1])};
+            l[0] *= f[0];
+            l[1] *= f[1];
+#pragma unroll
+            for (int i = 0; i < 2 * DV16; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][e] *= f[e >> 1];
+            m[0] = mn[0];
+            m[1] = mn[1];
+        }
+        // P as A fragments (the layout of S as it is), split into a bf16 value and its remainder
+        uint32_t ph[4], pl[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float p0 = attn::ex2(s[h][2 * r] - m[r]), p1 = attn::ex2(s[h][2 * r + 1] - m[r]);
+                l[r] += p0 + p1;
+                const uint32_t hi = pack_bf16x2(p0, p1);
+                ph[2 * h + r] = hi;
+                pl[2 * h + r] = pack_bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
+            }
+        // O += P V: V rows are the K axis of B, read transposed; a x4 load brings 16 slots of 16 columns
+        const uint32_t va = vd + (lane & 15) * vrb + 16 * (lane >> 4);
+#pragma unroll
+        for (int i = 0; i < DV16; ++i)
+            if (i < nv) {
+                uint32_t f[4];
+                ldsm4t(f, va + 32 * i);
+                mma16816(o[2 * i], ph, f[0], f[1]);
+                mma16816(o[2 * i], pl, f[0], f[1]);
+                mma16816(o[2 * i + 1], ph, f[2], f[3]);
+                mma16816(o[2 * i + 1], pl, f[2], f[3]);
+            }
     }
-    r.store(a.out + ((long long)b * a.Hq + h) * a.dv, a.dv, lane);
+    cp_wait<0>();
+    // the new token goes into the cache (one writer; no one reads that slot from it in this call)
+    if (g0 == 0 && slot / kSlots % stride == first) {
+        for (int i = lane; i < a.dk / 8; i += 32)
+            reinterpret_cast<uint4*>(kc + slot * kr)[i] = __ldg(reinterpret_cast<const uint4*>(kn) + i);
+        for (int i = lane; i < a.dv / 8; i += 32)
+            reinterpret_cast<uint4*>(vc + slot * vr)[i] = __ldg(reinterpret_cast<const uint4*>(vn) + i);
+    }
+
+    // ---- partial results: [warp][16 rows][m, l, O], then the CTA's over warp 0 .. kWarps - 1 ----
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    }
+    __syncthreads();                           // every warp is done with its ring
+    float* part = reinterpret_cast<float*>(smem);
+    const int pr = a.dv + 2, pw = kRows * pr;
+    {
+        float* w = part + (warp + 1) * pw;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float* row = w + ((lane >> 2) + 8 * r) * pr;
+            if ((lane & 3) == 0) {
+                row[0] = m[r];
+                row[1] = l[r];
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * DV16; ++i)
+                if (i < 2 * nv) {
+                    row[2 + 8 * i + 2 * (lane & 3)] = o[i][2 * r];
+                    row[3 + 8 * i + 2 * (lane & 3)] = o[i][2 * r + 1];
+                }
+        }
+    }
+    __syncthreads();
+    // merge the warps of this CTA into part 0; rows past the group's heads are not looked at
+    for (int i = tid; i < rows * a.dv; i += kThreads) {
+        const int r = i / a.dv, c = i - r * a.dv;
+        float M = -INFINITY, L = 0.0f, O = 0.0f;
+#pragma unroll
+        for (int w = 1; w <= kWarps; ++w) M = fmaxf(M, part[w * pw + r * pr]);
+#pragma unroll
+        for (int w = 1; w <= kWarps; ++w) {
+            const float* row = part + w * pw + r * pr;
+            const float f = row[0] == -INFINITY ? 0.0f : attn::ex2(row[0] - M);
+            L = fmaf(f, row[1], L);
+            O = fmaf(f, row[2 + c], O);
+        }
+        part[r * pr + 2 + c] = O;
+        if (c == 0) {
+            part[r * pr] = M;
+            part[r * pr + 1] = L;
+        }
+    }
+    if (X > 1) cluster_sync();
+    else __syncthreads();
+    // each CTA of the cluster finishes its share of the outputs
+    const uint32_t p0 = smem_u32(part);
+    __nv_bfloat16* out = a.out + ((long long)b * a.Hq + hk * G + g0) * a.dv;
+    for (int i = rank * kThreads + tid; i < rows * a.dv; i += X * kThreads) {
+        const int r = i / a.dv, c = i - r * a.dv;
+        float M = -INFINITY, L = 0.0f, O = 0.0f;
+        for (int k = 0; k < X; ++k) M = fmaxf(M, ld_remote(p0 + 4 * (r * pr), k));
+        for (int k = 0; k < X; ++k) {
+            const float mk = ld_remote(p0 + 4 * (r * pr), k);
+            const float f = mk == -INFINITY ? 0.0f : attn::ex2(mk - M);
+            L = fmaf(f, ld_remote(p0 + 4 * (r * pr + 1), k), L);
+            O = fmaf(f, ld_remote(p0 + 4 * (r * pr + 2 + c), k), O);
+        }
+        out[(long long)r * a.dv + c] = __float2bfloat16_rn(O / L);
+    }
+    if (X > 1) cluster_sync();                 // no CTA leaves while another reads its part
 }
+
+template <int DK16, int DV16>
+cudaError_t launch(const StepArgs& a, int X, cudaStream_t stream)
+{
+    const uint32_t smem = smem_bytes(a.dk, a.dv);
+    cudaError_t e = cudaFuncSetAttribute(window_step_kernel<DK16, DV16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem);
+    if (e != cudaSuccess) return e;
+    const int parts = (a.Hq / a.Hkv + kRows - 1) / kRows;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.Hkv * parts * X), (unsigned)a.B);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)X;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, window_step_kernel<DK16, DV16>, a);
+}
+
+}  // namespace step
 
 // Copies the tokens that stay visible (the sinks, and the window's last ones) into their
 // slots.  Block x takes one token, or, when the call has more tokens than the cache slots,
@@ -553,8 +788,19 @@ cudaError_t launch_window(const WindowArgs& a, cudaStream_t stream)
 
 cudaError_t launch_window_step(const StepArgs& a, cudaStream_t stream)
 {
-    window::window_step_kernel<<<dim3((unsigned)a.Hq, (unsigned)a.B), 32, 0, stream>>>(a);
-    return cudaGetLastError();
+    // CTAs per session and key head: double while the device would not be filled twice over, as long as
+    // each warp keeps a tile of its own
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const long long units = (long long)a.B * a.Hkv * ((a.Hq / a.Hkv + window::step::kRows - 1) / window::step::kRows);
+    const long long cap = (long long)a.window + a.sinks;
+    int X = 1;
+    while (X < 8 && units * X < sms && 2ll * X * window::step::kWarps * window::step::kSlots <= cap) X *= 2;
+    if (units * X / a.B > INT32_MAX) return cudaErrorInvalidValue;
+    if (a.dk <= 64 && a.dv <= 64) return window::step::launch<4, 4>(a, X, stream);
+    return window::step::launch<8, 8>(a, X, stream);
 }
 
 cudaError_t launch_window_append(const AppendArgs& a, cudaStream_t stream)
