@@ -32,6 +32,7 @@ struct StepArgs {
     __nv_bfloat16* out;                      // [B, Hq, dv]
     int B, Hq, Hkv, dk, dv, window, sinks;
     float scale;
+    uint64_t wait_limit_ns;
 };
 
 struct AppendArgs {
@@ -46,6 +47,21 @@ namespace window {
 
 __host__ __device__ __forceinline__ long long cache_slot(long long p, int window, int sinks) {
     return p < sinks ? p : sinks + (p - sinks) % window;
+}
+
+// 4-D bf16 map over a strided [B, T, H, d] tensor, box {64, 1, rows, 1}, 128-byte swizzle.
+bool make_map(CUtensorMap* map, const void* ptr, int d, int H, long long T, int B, int rows, long long head,
+              long long row, long long batch)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
+    cuuint64_t strides[3] = {(cuuint64_t)head * 2, (cuuint64_t)row * 2, (cuuint64_t)batch * 2};
+    cuuint32_t box[4] = {64, 1, (cuuint32_t)rows, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // ---- whole prompts: tcgen05 ----
@@ -407,21 +423,6 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
 }
 
-// 4-D bf16 map over a strided [B, T, H, d] tensor, box {64, 1, 128, 1}, 128-byte swizzle.
-bool make_map(CUtensorMap* map, const void* ptr, int d, int H, int T, int B, long long head, long long row,
-              long long batch)
-{
-    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
-    cuuint64_t strides[3] = {(cuuint64_t)head * 2, (cuuint64_t)row * 2, (cuuint64_t)batch * 2};
-    cuuint32_t box[4] = {64, 1, kBN, 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace tc
 
 // ---- one token per session ----
@@ -430,8 +431,9 @@ bool make_map(CUtensorMap* map, const void* ptr, int d, int H, int T, int B, lon
 // heads are the rows of mma.sync m16n8k16 tiles (tcgen05 takes 64 rows at least, of which a
 // group fills a few): with 16 slots a tile, a warp's scores, softmax and P V stay in its
 // registers, and a warp needs no other one until the end.  Each warp streams its tiles
-// (every warp of the cluster takes its turn) through a private ring of cp.async stages, so
-// kStages - 1 tiles per warp are in flight and no barrier stands in the loop.  The cluster's CTAs
+// (every warp of the cluster takes its turn) through a private ring of TMA boxes, so
+// kStages - 1 tiles per warp are in flight, a tile costs one thread a few instructions to fetch,
+// and no barrier of the CTA stands in the loop.  The cluster's CTAs
 // split one session and key head; the warps' partial sums (maximum, sum, O) meet in shared
 // memory, the CTAs' through distributed shared memory in a fixed order: one launch, no
 // workspace, the same bits every time.  P enters as a bf16 pair (value and remainder), since
@@ -442,14 +444,10 @@ using namespace sm100;
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kRows = 16, kSlots = 16;         // query heads, cache slots per tile
-constexpr int kStages = 4;
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
-    const int n = on ? 16 : 0;                 // 0 bytes read: the destination is filled with zeros
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+constexpr int kMaxCluster = 8;
+// Three stages and two CTAs per SM (96 KB of copies in flight at d 128); two stages and three CTAs
+// measured 139 against 138 us on 64 sessions of up to 4160 slots, 184 against 162 us on full ones.
+constexpr int kStages = 3, kCtas = 2;
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -477,28 +475,43 @@ __device__ __forceinline__ float ld_remote(uint32_t addr, uint32_t rank) {
     return v;
 }
 
-// Bytes of one stage (16 rows of K and of V; a row is padded by 16 bytes, so that the 8 rows of an
-// ldmatrix fall on different banks: d / 8 is even) and of the whole CTA.
-__host__ __device__ constexpr uint32_t row_bytes(int d) { return 2u * d + 16u; }
-__host__ __device__ constexpr uint32_t stage_bytes(int dk, int dv) { return kSlots * (row_bytes(dk) + row_bytes(dv)); }
+// One stage: 16 rows of K and of V as 64-column boxes of 16 x 128 bytes in the 128-byte swizzle,
+// under which the 8 rows of an ldmatrix fall on different banks.
+constexpr uint32_t kBox = kSlots * 128u;
+__host__ __device__ constexpr uint32_t boxes(int d) { return (uint32_t)(d + 63) / 64u; }
+__host__ __device__ constexpr uint32_t stage_bytes(int dk, int dv) { return kBox * (boxes(dk) + boxes(dv)); }
+__device__ __forceinline__ uint32_t chunk_offset(int row, int chunk) {      // of 16 bytes of a row
+    return (uint32_t)(chunk >> 3) * kBox + (uint32_t)row * 128u + (uint32_t)(((chunk & 7) ^ (row & 7)) << 4);
+}
 __host__ __device__ constexpr uint32_t part_floats(int dv) { return kRows * (dv + 2); }   // m, l and O of 16 rows
 __host__ __device__ constexpr uint32_t smem_bytes(int dk, int dv) {
     const uint32_t ring = kWarps * kStages * stage_bytes(dk, dv), parts = (kWarps + 1) * part_floats(dv) * 4;
-    return (ring > parts ? ring : parts);
+    return (ring > parts ? ring : parts) + 8u * kWarps * kStages + 16u + 1024u;   // + barriers, the abort flag, alignment
 }
 
-// DK16, DV16: the head sizes in units of 16, rounded up to what is instantiated (loops end at the
-// real ones).
+// DK16, DV16: the head sizes in units of 16, rounded up to whole boxes; the columns past a head's
+// size are zeros (the copies fill them, Q has zeros there) and are not stored.
 template <int DK16, int DV16>
-__global__ void __launch_bounds__(kThreads)
-window_step_kernel(const StepArgs a)
+__global__ void __launch_bounds__(kThreads, kCtas)
+window_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const StepArgs a)
 {
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int X = (int)cluster_size(), rank = (int)cluster_rank();
     const int G = a.Hq / a.Hkv, parts = (G + kRows - 1) / kRows;
     const int unit = blockIdx.x / X, hk = unit / parts, g0 = (unit % parts) * kRows, b = blockIdx.y;
     const long long pos = a.pos[b];
+    const uint32_t nbk = boxes(a.dk), nbv = boxes(a.dv), sb = stage_bytes(a.dk, a.dv);
+    const uint32_t ring = smem_u32(smem) + warp * kStages * sb;
+    const uint32_t tail = smem_bytes(a.dk, a.dv) - 8u * kWarps * kStages - 16u - 1024u;
+    const uint32_t bars = smem_u32(smem) + tail + 8u * kStages * warp;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + tail + 8u * kStages * kWarps);
+    if (lane < kStages) mbar_init(bars + 8u * lane, 1);
+    if (tid == 0) *abort_flag = 0;
+    fence_mbar_init();
+    __syncthreads();
     if (pos < 0) return;                       // idle: the whole cluster leaves
     const int cap = a.window + a.sinks;
     const int slot = (int)cache_slot(pos, a.window, a.sinks);
@@ -510,6 +523,21 @@ window_step_kernel(const StepArgs a)
     __nv_bfloat16* kc = a.k_cache + ((long long)b * cap * a.Hkv + hk) * a.dk;
     __nv_bfloat16* vc = a.v_cache + ((long long)b * cap * a.Hkv + hk) * a.dv;
     const long long kr = (long long)a.Hkv * a.dk, vr = (long long)a.Hkv * a.dv;
+
+    const int tiles = (seen + kSlots - 1) / kSlots, stride = X * kWarps, first = rank * kWarps + warp;
+    auto fetch = [&](int tile, int stage) {
+        if (lane == 0) {
+            const uint32_t dst = ring + stage * sb, bar = bars + 8u * stage;
+            mbar_arrive_expect_tx(bar, sb);
+            for (uint32_t c = 0; c < nbk; ++c) tma_load_4d(dst + c * kBox, &tm_k, bar, 64 * c, hk, tile * kSlots, b);
+            for (uint32_t c = 0; c < nbv; ++c)
+                tma_load_4d(dst + (nbk + c) * kBox, &tm_v, bar, 64 * c, hk, tile * kSlots, b);
+        }
+        __syncwarp();
+    };
+
+    int issued = 0, taken = 0;                 // tiles of this warp
+    for (; issued < kStages - 1 && first + issued * stride < tiles; ++issued) fetch(first + issued * stride, issued);
 
     // Q as A fragments: row r = lane / 4 (and + 8), columns 2 (lane % 4) (and + 8) of each 16
     uint32_t qa[DK16][4];
@@ -525,28 +553,6 @@ window_step_kernel(const StepArgs a)
             }
     }
 
-    const uint32_t sb = stage_bytes(a.dk, a.dv), krb = row_bytes(a.dk), vrb = row_bytes(a.dv);
-    const uint32_t ring = smem_u32(smem) + warp * kStages * sb;
-    const int tiles = (seen + kSlots - 1) / kSlots, stride = X * kWarps, first = rank * kWarps + warp;
-    // slots past the last one seen are filled with zeros, not read; the new token's rows come from k and v
-    auto fetch = [&](int tile, int stage) {
-        const uint32_t kd = ring + stage * sb, vd = kd + kSlots * krb;
-        if (tile < tiles) {
-            const int ck = a.dk / 8, cv = a.dv / 8;
-            for (int i = lane; i < kSlots * ck; i += 32) {
-                const int r = i / ck, c = i - r * ck, s = tile * kSlots + r;
-                const __nv_bfloat16* src = s == slot ? kn : kc + (s < seen ? s : 0) * kr;
-                cp_async16(kd + r * krb + 16 * c, src + 8 * c, s < seen);
-            }
-            for (int i = lane; i < kSlots * cv; i += 32) {
-                const int r = i / cv, c = i - r * cv, s = tile * kSlots + r;
-                const __nv_bfloat16* src = s == slot ? vn : vc + (s < seen ? s : 0) * vr;
-                cp_async16(vd + r * vrb + 16 * c, src + 8 * c, s < seen);
-            }
-        }
-        cp_commit();
-    };
-
     float o[2 * DV16][4];
 #pragma unroll
     for (int i = 0; i < 2 * DV16; ++i)
@@ -555,26 +561,50 @@ window_step_kernel(const StepArgs a)
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};     // rows lane / 4 and + 8; l: this thread's columns
     const float sc = a.scale * 1.4426950408889634f;
 
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(first + i * stride, i);
-    int st = 0;
+    // this lane's rows of an ldmatrix: the 16-byte chunk of step i is this one with bits 5 and 6 flipped by i
+    const uint32_t ka0 = chunk_offset((lane & 7) + 8 * (lane >> 4), (lane >> 3) & 1);
+    const uint32_t va0 = chunk_offset(lane & 15, lane >> 4);
     for (int tile = first; tile < tiles; tile += stride) {
-        cp_wait<kStages - 2>();
-        __syncwarp();
-        fetch(tile + (kStages - 1) * stride, st == 0 ? kStages - 1 : st - 1);
-        const uint32_t kd = ring + st * sb, vd = kd + kSlots * krb;
-        st = st + 1 == kStages ? 0 : st + 1;
-        // S [16 x 16] = Q K^T: K rows are the columns of B; a x4 load brings slots 0-7 and 8-15, both halves of 16 d
-        float s[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-        const uint32_t ka = kd + ((lane & 7) + 8 * (lane >> 4)) * krb + 16 * ((lane >> 3) & 1);
-#pragma unroll
-        for (int i = 0; i < DK16; ++i)
-            if (i < nk) {
-                uint32_t f[4];
-                ldsm4(f, ka + 32 * i);
-                mma16816(s[0], qa[i], f[0], f[1]);
-                mma16816(s[1], qa[i], f[2], f[3]);
+        const int st = taken % kStages;
+        if (!__all_sync(0xffffffffu, mbar_wait(bars + 8u * st, (uint32_t)(taken / kStages) & 1u, abort_flag, a.wait_limit_ns, 51)))
+            break;
+        ++taken;
+        // the stage read last (its reads are over for the whole warp) takes the next tile
+        if (first + issued * stride < tiles) {
+            fetch(first + issued * stride, issued % kStages);
+            ++issued;
+        }
+        const uint32_t kd = ring + st * sb, vd = kd + nbk * kBox;
+        // The copy may have brought what must not count: the new token's rows stand in k and v, not in
+        // their slot, and V rows past the last slot seen (zero times which must be zero) hold anything.
+        const int mine = slot - tile * kSlots, past = seen - tile * kSlots;
+        if ((mine >= 0 && mine < kSlots) || past < kSlots) {
+            if (mine >= 0 && mine < kSlots) {
+                for (int c = lane; c < a.dk / 8; c += 32) {
+                    const uint4 w = __ldg(reinterpret_cast<const uint4*>(kn) + c);
+                    st_shared_v4(kd + chunk_offset(mine, c), w.x, w.y, w.z, w.w);
+                }
+                for (int c = lane; c < a.dv / 8; c += 32) {
+                    const uint4 w = __ldg(reinterpret_cast<const uint4*>(vn) + c);
+                    st_shared_v4(vd + chunk_offset(mine, c), w.x, w.y, w.z, w.w);
+                }
             }
+            for (int i = max(past, 0) * 8 + lane; i < kSlots * 8; i += 32)
+                for (uint32_t c = 0; c < nbv; ++c) st_shared_v4(vd + c * kBox + 16u * i, 0, 0, 0, 0);
+            fence_proxy_async_smem();          // before a later copy into this stage
+            __syncwarp();
+        }
+        // S [16 x 16] = Q K^T: K rows are the columns of B; a x4 load brings slots 0-7 and 8-15, both halves of 16 d
+        // (two sums of every other 16 d: half as long a chain of dependent products)
+        float s[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}}, s2[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        const uint32_t ka = kd + ka0;
+#pragma unroll
+        for (int i = 0; i < DK16; ++i) {
+            uint32_t f[4];
+            ldsm4(f, (ka ^ (uint32_t)((i & 3) << 5)) + (i >> 2) * kBox);
+            mma16816((i & 1) ? s2[0] : s[0], qa[i], f[0], f[1]);
+            mma16816((i & 1) ? s2[1] : s[1], qa[i], f[2], f[3]);
+        }
         // online softmax of this warp's slots; columns 2 (lane % 4) + {0, 1} of each 8
         const int left = seen - tile * kSlots;
         float mt[2] = {-INFINITY, -INFINITY};
@@ -583,7 +613,7 @@ window_step_kernel(const StepArgs a)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int col = 8 * h + 2 * (lane & 3) + (e & 1);
-                s[h][e] = col < left ? s[h][e] * sc : -INFINITY;
+                s[h][e] = col < left ? (s[h][e] + s2[h][e]) * sc : -INFINITY;
                 mt[e >> 1] = fmaxf(mt[e >> 1], s[h][e]);
             }
 #pragma unroll
@@ -616,19 +646,21 @@ window_step_kernel(const StepArgs a)
                 pl[2 * h + r] = pack_bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
             }
         // O += P V: V rows are the K axis of B, read transposed; a x4 load brings 16 slots of 16 columns
-        const uint32_t va = vd + (lane & 15) * vrb + 16 * (lane >> 4);
+        const uint32_t va = vd + va0;
 #pragma unroll
-        for (int i = 0; i < DV16; ++i)
-            if (i < nv) {
-                uint32_t f[4];
-                ldsm4t(f, va + 32 * i);
-                mma16816(o[2 * i], ph, f[0], f[1]);
-                mma16816(o[2 * i], pl, f[0], f[1]);
-                mma16816(o[2 * i + 1], ph, f[2], f[3]);
-                mma16816(o[2 * i + 1], pl, f[2], f[3]);
-            }
+        for (int i = 0; i < DV16; ++i) {
+            uint32_t f[4];
+            ldsm4t(f, (va ^ (uint32_t)((i & 3) << 5)) + (i >> 2) * kBox);
+            mma16816(o[2 * i], ph, f[0], f[1]);
+            mma16816(o[2 * i + 1], ph, f[2], f[3]);
+            mma16816(o[2 * i], pl, f[0], f[1]);
+            mma16816(o[2 * i + 1], pl, f[2], f[3]);
+        }
     }
-    cp_wait<0>();
+    // after a wait that gave up: the copies in flight land before the ring is used for anything else
+    if (lane == 0)
+        for (int i = taken; i < issued; ++i) drain_wait(bars + 8u * (i % kStages), (uint32_t)(i / kStages) & 1u);
+    __syncwarp();
     // the new token goes into the cache (one writer; no one reads that slot from it in this call)
     if (g0 == 0 && slot / kSlots % stride == first) {
         for (int i = lane; i < a.dk / 8; i += 32)
@@ -650,6 +682,7 @@ window_step_kernel(const StepArgs a)
         float* w = part + (warp + 1) * pw;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
+            if ((lane >> 2) + 8 * r >= rows) continue;
             float* row = w + ((lane >> 2) + 8 * r) * pr;
             if ((lane & 3) == 0) {
                 row[0] = m[r];
@@ -691,12 +724,20 @@ window_step_kernel(const StepArgs a)
     for (int i = rank * kThreads + tid; i < rows * a.dv; i += X * kThreads) {
         const int r = i / a.dv, c = i - r * a.dv;
         float M = -INFINITY, L = 0.0f, O = 0.0f;
-        for (int k = 0; k < X; ++k) M = fmaxf(M, ld_remote(p0 + 4 * (r * pr), k));
-        for (int k = 0; k < X; ++k) {
-            const float mk = ld_remote(p0 + 4 * (r * pr), k);
-            const float f = mk == -INFINITY ? 0.0f : attn::ex2(mk - M);
-            L = fmaf(f, ld_remote(p0 + 4 * (r * pr + 1), k), L);
-            O = fmaf(f, ld_remote(p0 + 4 * (r * pr + 2 + c), k), O);
+        float mk[kMaxCluster], lk[kMaxCluster], ok[kMaxCluster];
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k) {          // all loads on their way before the first is used
+            mk[k] = k < X ? ld_remote(p0 + 4 * (r * pr), k) : -INFINITY;
+            lk[k] = k < X ? ld_remote(p0 + 4 * (r * pr + 1), k) : 0.0f;
+            ok[k] = k < X ? ld_remote(p0 + 4 * (r * pr + 2 + c), k) : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k) M = fmaxf(M, mk[k]);
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k) {
+            const float f = mk[k] == -INFINITY ? 0.0f : attn::ex2(mk[k] - M);
+            L = fmaf(f, lk[k], L);
+            O = fmaf(f, ok[k], O);
         }
         out[(long long)r * a.dv + c] = __float2bfloat16_rn(O / L);
     }
@@ -707,6 +748,11 @@ template <int DK16, int DV16>
 cudaError_t launch(const StepArgs& a, int X, cudaStream_t stream)
 {
     const uint32_t smem = smem_bytes(a.dk, a.dv);
+    CUtensorMap mk, mv;
+    const long long slots = (long long)a.window + a.sinks, H = a.Hkv;
+    if (!make_map(&mk, a.k_cache, a.dk, a.Hkv, slots, a.B, kSlots, a.dk, H * a.dk, slots * H * a.dk) ||
+        !make_map(&mv, a.v_cache, a.dv, a.Hkv, slots, a.B, kSlots, a.dv, H * a.dv, slots * H * a.dv))
+        return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(window_step_kernel<DK16, DV16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
     if (e != cudaSuccess) return e;
@@ -722,7 +768,7 @@ cudaError_t launch(const StepArgs& a, int X, cudaStream_t stream)
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, window_step_kernel<DK16, DV16>, a);
+    return cudaLaunchKernelEx(&cfg, window_step_kernel<DK16, DV16>, mk, mv, a);
 }
 
 }  // namespace step
@@ -762,9 +808,9 @@ cudaError_t launch_window(const WindowArgs& a, cudaStream_t stream)
 {
     using namespace window::tc;
     CUtensorMap mq, mk, mv;
-    if (!make_map(&mq, a.q, a.dk, a.Hq, a.Tq, a.B, a.q_head, a.q_row, a.q_batch) ||
-        !make_map(&mk, a.k, a.dk, a.Hkv, a.Tk, a.B, a.k_head, a.k_row, a.k_batch) ||
-        !make_map(&mv, a.v, a.dv, a.Hkv, a.Tk, a.B, a.v_head, a.v_row, a.v_batch))
+    if (!window::make_map(&mq, a.q, a.dk, a.Hq, a.Tq, a.B, kBM, a.q_head, a.q_row, a.q_batch) ||
+        !window::make_map(&mk, a.k, a.dk, a.Hkv, a.Tk, a.B, kBM, a.k_head, a.k_row, a.k_batch) ||
+        !window::make_map(&mv, a.v, a.dv, a.Hkv, a.Tk, a.B, kBM, a.v_head, a.v_row, a.v_batch))
         return cudaErrorInvalidValue;
     // (a per-device setting of the current context: set on every call)
     cudaError_t e = cudaFuncSetAttribute(window_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
@@ -788,19 +834,23 @@ cudaError_t launch_window(const WindowArgs& a, cudaStream_t stream)
 
 cudaError_t launch_window_step(const StepArgs& a, cudaStream_t stream)
 {
-    // CTAs per session and key head: double while the device would not be filled twice over, as long as
-    // each warp keeps a tile of its own
+    // CTAs per session and key head: doubled while they all fit on the device at once (two per SM) and
+    // each warp keeps a tile of its own.  Beyond one wave splitting loses: 64 sessions of 4160 slots on
+    // 8 key heads (512 units) take 162 us unsplit and 177 us in halves; 16 sessions of 32,832 slots
+    // (128 units) 425 us unsplit and 306 us in halves.
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
+    StepArgs r = a;
+    r.wait_limit_ns = g_wait_limit_ns;
     const long long units = (long long)a.B * a.Hkv * ((a.Hq / a.Hkv + window::step::kRows - 1) / window::step::kRows);
     const long long cap = (long long)a.window + a.sinks;
     int X = 1;
-    while (X < 8 && units * X < sms && 2ll * X * window::step::kWarps * window::step::kSlots <= cap) X *= 2;
+    while (X < window::step::kMaxCluster && units * X <= sms && 2ll * X * window::step::kWarps * window::step::kSlots <= cap) X *= 2;
     if (units * X / a.B > INT32_MAX) return cudaErrorInvalidValue;
-    if (a.dk <= 64 && a.dv <= 64) return window::step::launch<4, 4>(a, X, stream);
-    return window::step::launch<8, 8>(a, X, stream);
+    if (a.dk <= 64) return a.dv <= 64 ? window::step::launch<4, 4>(r, X, stream) : window::step::launch<4, 8>(r, X, stream);
+    return a.dv <= 64 ? window::step::launch<8, 4>(r, X, stream) : window::step::launch<8, 8>(r, X, stream);
 }
 
 cudaError_t launch_window_append(const AppendArgs& a, cudaStream_t stream)

@@ -510,19 +510,27 @@ def test_captured_and_replayed_beside_eager_calls(cuda):
         assert torch.equal(kc, kv[0]) and torch.equal(vc, kv[1])
 
 
-def test_window_attention_timeout_is_reported_and_recovers(cuda):
+@pytest.mark.parametrize("step", [False, True])
+def test_window_attention_timeout_is_reported_and_recovers(cuda, step):
     """A wait that runs out (the bound shortened to 1 ns) is reported, and the next call is right."""
     g = gen(12)
-    q, k, v = attn_inputs(g, 1, 2000, 2000, 4, 2, 112, 112)
-    want = G.window_attention(q, k, v, 500, 20)
+    if step:
+        q, k, v = attn_inputs(g, 2, 1, 1, 8, 2, 112, 112)
+        kc, vc = normal(g, 2, 2010, 2, 112, dtype=torch.bfloat16), normal(g, 2, 2010, 2, 112, dtype=torch.bfloat16)
+        pos = torch.tensor([5000, 1700], dtype=torch.int32, device=cuda)
+        call = lambda: G.window_attention_step(q[:, 0], k[:, 0], v[:, 0], kc, vc, pos, 2000, 10)
+    else:
+        q, k, v = attn_inputs(g, 1, 2000, 2000, 4, 2, 112, 112)
+        call = lambda: G.window_attention(q, k, v, 500, 20)
+    want = call()
     done()
     try:
         G.gdn_set_wait_limit_ns(1)
-        G.window_attention(q, k, v, 500, 20)
+        call()
         assert G.gdn_get_last_device_status() == G.GDN_ERR_TIMEOUT
     finally:
         G.gdn_set_wait_limit_ns(0)
-    got = G.window_attention(q, k, v, 500, 20)
+    got = call()
     done()
     assert torch.equal(got, want)
 
