@@ -30,11 +30,16 @@ _ARGTYPES = {
 }
 
 _fns = {}
+_torch = None
 
 
 def _fn(name):
+    """The library's entry, with its argument types set (and torch at hand: callers hold tensors)."""
+    global _torch
     f = _fns.get(name)
     if f is None:
+        import torch
+        _torch = torch
         f = getattr(_gdn.load(), name)
         f.argtypes, f.restype = _ARGTYPES[name], _I
         _fns[name] = f
@@ -43,13 +48,12 @@ def _fn(name):
 
 def _call(name, device, *args):
     """One library call on the current stream of ``device`` (made current for it)."""
-    import torch
-    index = device.index
-    if index == torch.cuda.current_device():
-        st = _fn(name)(*args, torch._C._cuda_getCurrentRawStream(index))
+    f, cuda, index = _fn(name), _torch.cuda, device.index
+    if index == cuda.current_device():
+        st = f(*args, _torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(index):
-            st = _fn(name)(*args, torch._C._cuda_getCurrentRawStream(index))
+        with cuda.device(index):
+            st = f(*args, _torch._C._cuda_getCurrentRawStream(index))
     if st:
         raise _gdn.GdnError(st, name)
 
@@ -59,74 +63,82 @@ def _need(cond, what):
         raise ValueError(what)
 
 
-def _tensor(t, name, shape, dtype, device, contiguous=True):
-    """``t`` has this shape, type and device, and rows contiguous in the last dimension."""
+def _mismatch(t, name, shape, dtype, device):
+    raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _rows(t, name, shape, dtype, device):
+    """Pointer and strides of a tensor of this shape, type and device, contiguous in its last dimension."""
     if t.shape != shape or t.dtype is not dtype or t.device != device:
-        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {device}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    if contiguous:
-        _need(t.is_contiguous(), f"{name} must be contiguous")
-    else:
-        _need(t.stride(-1) == 1 or t.shape[-1] == 1, f"{name} must be contiguous in its last dimension")
+        _mismatch(t, name, shape, dtype, device)
+    s = t.stride()
+    if s[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return t.data_ptr(), s
 
 
-def _opt(t, name, shape, dtype, device):
+def _whole(t, name, shape, dtype, device):
+    """Pointer of a contiguous tensor of this shape, type and device; None stays None."""
     if t is None:
         return None
-    _tensor(t, name, shape, dtype, device)
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        _mismatch(t, name, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _suffix(t, name):
-    import torch
+def _new(out, name, like, shape, dtype, lengths=None):
+    """``out`` after its checks, or a new tensor on the device of ``like`` (zeros where padding stays)."""
+    if out is None:
+        return like.new_empty(shape, dtype=dtype) if lengths is None else like.new_zeros(shape, dtype=dtype)
+    _need(out.device == like.device, f"{name} must be on {like.device}")
+    _whole(out, name, shape, dtype, like.device)
+    return out
+
+
+def _types(t, name, entry):
+    """The entry for a tensor's element type, bfloat16 or float32; its device and types."""
+    _fn(entry)
+    dtype, f32 = t.dtype, _torch.float32
     _need(t.is_cuda, f"{name} must be on a CUDA device")
-    if t.dtype is torch.bfloat16:
-        return ""
-    _need(t.dtype is torch.float32, f"{name} must be bfloat16 or float32, got {t.dtype}")
-    return "_f32"
+    _need(dtype is f32 or dtype is _torch.bfloat16, f"{name} must be bfloat16 or float32, got {dtype}")
+    return (entry + "_f32" if dtype is f32 else entry), t.device, dtype, f32, _torch.int32
 
 
-def _new(out, name, shape, dtype, device, lengths):
-    import torch
-    if out is not None:
-        _tensor(out, name, shape, dtype, device)
-        return out
-    make = torch.empty if lengths is None else torch.zeros
-    return make(shape, dtype=dtype, device=device)
+def _bf16(t, name, entry):
+    _fn(entry)
+    dtype = _torch.bfloat16
+    _need(t.is_cuda and t.dtype is dtype, f"{name} must be bfloat16 on a CUDA device")
+    return t.device, dtype, _torch.int32
 
 
 def causal_conv(x, weight, bias=None, state=None, silu=True, lengths=None, out=None, state_out=None):
     """out, state_out of the causal depthwise convolution of x [B, T, D] with weight [D, width]
     (float32, width 2 to 4); state [B, width - 1, D] holds the inputs before the call (None:
     zeros).  ``state_out`` may be ``state`` itself."""
-    import torch
-    sfx = _suffix(x, "x")
-    dev, dt = x.device, x.dtype
+    name, dev, ty, f32, i32 = _types(x, "x", "gdn_causal_conv")
     B, T, D = x.shape
     W = weight.shape[1]
-    _tensor(x, "x", x.shape, dt, dev, contiguous=False)
-    _tensor(weight, "weight", (D, W), torch.float32, dev)
-    out = _new(out, "out", (B, T, D), dt, dev, lengths)
-    state_out = _new(state_out, "state_out", (B, W - 1, D), dt, dev, None)
-    _call("gdn_causal_conv" + sfx, dev, x.data_ptr(), x.stride(0), x.stride(1), weight.data_ptr(),
-          _opt(bias, "bias", (D,), torch.float32, dev), _opt(state, "state", (B, W - 1, D), dt, dev),
-          state_out.data_ptr(), _opt(lengths, "lengths", (B,), torch.int32, dev), out.data_ptr(), B, T, D, W, int(silu))
+    xp, xs = _rows(x, "x", x.shape, ty, dev)
+    wp, bp = _whole(weight, "weight", (D, W), f32, dev), _whole(bias, "bias", (D,), f32, dev)
+    sp, lp = _whole(state, "state", (B, W - 1, D), ty, dev), _whole(lengths, "lengths", (B,), i32, dev)
+    out = _new(out, "out", x, (B, T, D), ty, lengths)
+    state_out = _new(state_out, "state_out", x, (B, W - 1, D), ty)
+    _call(name, dev, xp, xs[0], xs[1], wp, bp, sp, state_out.data_ptr(), lp, out.data_ptr(), B, T, D, W, int(silu))
     return out, state_out
 
 
 def causal_conv_step(x, weight, bias, state, silu=True, out=None):
     """out [B, D] for one token x [B, D]; state [B, width - 1, D] is advanced in place."""
-    import torch
-    sfx = _suffix(x, "x")
-    dev, dt = x.device, x.dtype
+    name, dev, ty, f32, _ = _types(x, "x", "gdn_causal_conv_step")
     B, D = x.shape
     W = weight.shape[1]
-    _tensor(x, "x", x.shape, dt, dev, contiguous=False)
-    _tensor(weight, "weight", (D, W), torch.float32, dev)
-    _tensor(state, "state", (B, W - 1, D), dt, dev)
-    out = _new(out, "out", (B, D), dt, dev, None)
-    _call("gdn_causal_conv_step" + sfx, dev, x.data_ptr(), x.stride(0), weight.data_ptr(),
-          _opt(bias, "bias", (D,), torch.float32, dev), state.data_ptr(), out.data_ptr(), B, D, W, int(silu))
+    xp, xs = _rows(x, "x", x.shape, ty, dev)
+    wp, bp = _whole(weight, "weight", (D, W), f32, dev), _whole(bias, "bias", (D,), f32, dev)
+    sp = _whole(state, "state", (B, W - 1, D), ty, dev)
+    out = _new(out, "out", x, (B, D), ty)
+    _call(name, dev, xp, xs[0], wp, bp, sp, out.data_ptr(), B, D, W, int(silu))
     return out
 
 
@@ -134,78 +146,56 @@ def selective_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, state=None, d
                    out=None, state_out=None):
     """y [B, T, D], state_out [B, D, N] of the selective scan of x, dt, z [B, T, D] with A [D, N]
     (float32) and Bm, Cm [B, T, N]; state (float32 [B, D, N], None: zeros) may be ``state_out``."""
-    import torch
-    sfx = _suffix(x, "x")
-    dev, ty = x.device, x.dtype
+    name, dev, ty, f32, i32 = _types(x, "x", "gdn_selective_scan")
     B, T, E = x.shape
     N = A.shape[1]
-    _tensor(x, "x", x.shape, ty, dev, contiguous=False)
-    _tensor(dt, "dt", x.shape, ty, dev, contiguous=False)
-    _tensor(A, "A", (E, N), torch.float32, dev)
-    _tensor(Bm, "Bm", (B, T, N), ty, dev, contiguous=False)
-    _tensor(Cm, "Cm", (B, T, N), ty, dev, contiguous=False)
-    zp = (None, 0, 0)
-    if z is not None:
-        _tensor(z, "z", x.shape, ty, dev, contiguous=False)
-        zp = (z.data_ptr(), z.stride(0), z.stride(1))
-    y = _new(out, "out", (B, T, E), ty, dev, lengths)
-    state_out = _new(state_out, "state_out", (B, E, N), torch.float32, dev, None)
-    _call("gdn_selective_scan" + sfx, dev, x.data_ptr(), x.stride(0), x.stride(1), dt.data_ptr(), dt.stride(0),
-          dt.stride(1), A.data_ptr(), Bm.data_ptr(), Bm.stride(0), Bm.stride(1), Cm.data_ptr(), Cm.stride(0),
-          Cm.stride(1), _opt(D, "D", (E,), torch.float32, dev), *zp,
-          _opt(dt_bias, "dt_bias", (E,), torch.float32, dev), _opt(state, "state", (B, E, N), torch.float32, dev),
-          state_out.data_ptr(), _opt(lengths, "lengths", (B,), torch.int32, dev), y.data_ptr(), B, T, E, N,
-          int(dt_softplus))
+    xp, xs = _rows(x, "x", x.shape, ty, dev)
+    dp, ds = _rows(dt, "dt", x.shape, ty, dev)
+    bp, bs = _rows(Bm, "Bm", (B, T, N), ty, dev)
+    cp, cs = _rows(Cm, "Cm", (B, T, N), ty, dev)
+    zp, zs = (None, (0, 0)) if z is None else _rows(z, "z", x.shape, ty, dev)
+    ap, kp = _whole(A, "A", (E, N), f32, dev), _whole(D, "D", (E,), f32, dev)
+    tp, sp = _whole(dt_bias, "dt_bias", (E,), f32, dev), _whole(state, "state", (B, E, N), f32, dev)
+    lp = _whole(lengths, "lengths", (B,), i32, dev)
+    y = _new(out, "out", x, (B, T, E), ty, lengths)
+    state_out = _new(state_out, "state_out", x, (B, E, N), f32)
+    _call(name, dev, xp, xs[0], xs[1], dp, ds[0], ds[1], ap, bp, bs[0], bs[1], cp, cs[0], cs[1], kp, zp, zs[0], zs[1],
+          tp, sp, state_out.data_ptr(), lp, y.data_ptr(), B, T, E, N, int(dt_softplus))
     return y, state_out
 
 
 def selective_scan_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, dt_softplus=True, out=None):
     """y [B, D] for one token (x, dt, z [B, D]; Bm, Cm [B, N]); state [B, D, N] advances in place."""
-    import torch
-    sfx = _suffix(x, "x")
-    dev, ty = x.device, x.dtype
+    name, dev, ty, f32, _ = _types(x, "x", "gdn_selective_scan_step")
     B, E = x.shape
     N = A.shape[1]
-    _tensor(x, "x", x.shape, ty, dev, contiguous=False)
-    _tensor(dt, "dt", x.shape, ty, dev, contiguous=False)
-    _tensor(A, "A", (E, N), torch.float32, dev)
-    _tensor(Bm, "Bm", (B, N), ty, dev, contiguous=False)
-    _tensor(Cm, "Cm", (B, N), ty, dev, contiguous=False)
-    _tensor(state, "state", (B, E, N), torch.float32, dev)
-    zp = (None, 0)
-    if z is not None:
-        _tensor(z, "z", x.shape, ty, dev, contiguous=False)
-        zp = (z.data_ptr(), z.stride(0))
-    y = _new(out, "out", (B, E), ty, dev, None)
-    _call("gdn_selective_scan_step" + sfx, dev, x.data_ptr(), x.stride(0), dt.data_ptr(), dt.stride(0), A.data_ptr(),
-          Bm.data_ptr(), Bm.stride(0), Cm.data_ptr(), Cm.stride(0), _opt(D, "D", (E,), torch.float32, dev), *zp,
-          _opt(dt_bias, "dt_bias", (E,), torch.float32, dev), state.data_ptr(), y.data_ptr(), B, E, N,
+    xp, xs = _rows(x, "x", x.shape, ty, dev)
+    dp, ds = _rows(dt, "dt", x.shape, ty, dev)
+    bp, bs = _rows(Bm, "Bm", (B, N), ty, dev)
+    cp, cs = _rows(Cm, "Cm", (B, N), ty, dev)
+    zp, zs = (None, (0,)) if z is None else _rows(z, "z", x.shape, ty, dev)
+    ap, kp = _whole(A, "A", (E, N), f32, dev), _whole(D, "D", (E,), f32, dev)
+    tp, sp = _whole(dt_bias, "dt_bias", (E,), f32, dev), _whole(state, "state", (B, E, N), f32, dev)
+    y = _new(out, "out", x, (B, E), ty)
+    _call(name, dev, xp, xs[0], dp, ds[0], ap, bp, bs[0], cp, cs[0], kp, zp, zs[0], tp, sp, y.data_ptr(), B, E, N,
           int(dt_softplus))
     return y
-
-
-def _bf16(t, name):
-    import torch
-    _need(t.is_cuda and t.dtype is torch.bfloat16, f"{name} must be bfloat16 on a CUDA device")
 
 
 def window_attention(q, k, v, window, sinks=0, lengths=None, scale=None, out=None):
     """out [B, Tq, Hq, d_v]: softmax attention of q [B, Tq, Hq, d_k], the last Tq of the Tk tokens
     of k [B, Tk, Hkv, d_k] and v [B, Tk, Hkv, d_v], over each token's last ``window`` tokens
     (itself among them) and the first ``sinks``.  ``scale`` is 1 / sqrt(d_k) unless given."""
-    import torch
-    _bf16(q, "q")
-    dev, ty = q.device, q.dtype
+    dev, ty, i32 = _bf16(q, "q", "gdn_window_attention")
     B, Tq, Hq, dk = q.shape
     _, Tk, Hkv, dv = v.shape
-    _tensor(q, "q", q.shape, ty, dev, contiguous=False)
-    _tensor(k, "k", (B, Tk, Hkv, dk), ty, dev, contiguous=False)
-    _tensor(v, "v", (B, Tk, Hkv, dv), ty, dev, contiguous=False)
-    out = _new(out, "out", (B, Tq, Hq, dv), ty, dev, lengths)
-    _call("gdn_window_attention", dev, q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), k.data_ptr(), k.stride(0),
-          k.stride(1), k.stride(2), v.data_ptr(), v.stride(0), v.stride(1), v.stride(2),
-          _opt(lengths, "lengths", (B,), torch.int32, dev), out.data_ptr(), B, Tq, Tk, Hq, Hkv, dk, dv, window, sinks,
-          dk ** -0.5 if scale is None else scale)
+    qp, qs = _rows(q, "q", q.shape, ty, dev)
+    kp, ks = _rows(k, "k", (B, Tk, Hkv, dk), ty, dev)
+    vp, vs = _rows(v, "v", (B, Tk, Hkv, dv), ty, dev)
+    lp = _whole(lengths, "lengths", (B,), i32, dev)
+    out = _new(out, "out", q, (B, Tq, Hq, dv), ty, lengths)
+    _call("gdn_window_attention", dev, qp, qs[0], qs[1], qs[2], kp, ks[0], ks[1], ks[2], vp, vs[0], vs[1], vs[2], lp,
+          out.data_ptr(), B, Tq, Tk, Hq, Hkv, dk, dv, window, sinks, dk ** -0.5 if scale is None else scale)
     return out
 
 
@@ -215,48 +205,42 @@ def window_cache(B, Hkv, d_k, d_v, window, sinks=0, device="cuda"):
     return tuple(torch.empty((B, window + sinks, Hkv, d), dtype=torch.bfloat16, device=device) for d in (d_k, d_v))
 
 
-def _heads_row(t, name):
-    _need(t.stride(-2) == t.shape[-1] or t.shape[-2] == 1, f"{name}: a token's heads must be contiguous")
+def _token(t, name, shape, dtype, device):
+    """As _rows, a token's heads contiguous."""
+    p, s = _rows(t, name, shape, dtype, device)
+    if s[-2] != shape[-1] and shape[-2] != 1:
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return p, s
 
 
 def window_cache_append(k, v, k_cache, v_cache, start, window, sinks=0, lengths=None):
     """Copy the tokens of k, v [B, T, Hkv, d] that stay visible into the rolling caches, as tokens
     start[b] .. of each session (``start`` int32 [B], None: 0)."""
-    import torch
-    _bf16(k, "k")
-    dev, ty = k.device, k.dtype
+    dev, ty, i32 = _bf16(k, "k", "gdn_window_cache_append")
     B, T, Hkv, dk = k.shape
     dv = v.shape[3]
-    _tensor(k, "k", k.shape, ty, dev, contiguous=False)
-    _tensor(v, "v", (B, T, Hkv, dv), ty, dev, contiguous=False)
-    _heads_row(k, "k")
-    _heads_row(v, "v")
-    _tensor(k_cache, "k_cache", (B, window + sinks, Hkv, dk), ty, dev)
-    _tensor(v_cache, "v_cache", (B, window + sinks, Hkv, dv), ty, dev)
-    _call("gdn_window_cache_append", dev, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-          v.stride(1), k_cache.data_ptr(), v_cache.data_ptr(), _opt(start, "start", (B,), torch.int32, dev),
-          _opt(lengths, "lengths", (B,), torch.int32, dev), B, T, Hkv, dk, dv, window, sinks)
+    kp, ks = _token(k, "k", k.shape, ty, dev)
+    vp, vs = _token(v, "v", (B, T, Hkv, dv), ty, dev)
+    kc = _whole(k_cache, "k_cache", (B, window + sinks, Hkv, dk), ty, dev)
+    vc = _whole(v_cache, "v_cache", (B, window + sinks, Hkv, dv), ty, dev)
+    sp, lp = _whole(start, "start", (B,), i32, dev), _whole(lengths, "lengths", (B,), i32, dev)
+    _call("gdn_window_cache_append", dev, kp, ks[0], ks[1], vp, vs[0], vs[1], kc, vc, sp, lp, B, T, Hkv, dk, dv, window,
+          sinks)
 
 
 def window_attention_step(q, k, v, k_cache, v_cache, pos, window, sinks=0, scale=None, out=None):
     """out [B, Hq, d_v] for one token per session: k, v [B, Hkv, d] go into the rolling caches as
     token pos[b] (int32 [B]; negative: an idle session) and q [B, Hq, d_k] attends over them."""
-    import torch
-    _bf16(q, "q")
-    dev, ty = q.device, q.dtype
+    dev, ty, i32 = _bf16(q, "q", "gdn_window_attention_step")
     B, Hq, dk = q.shape
-    Hkv, dv = v.shape[1], v.shape[2]
-    _tensor(q, "q", q.shape, ty, dev, contiguous=False)
-    _tensor(k, "k", (B, Hkv, dk), ty, dev, contiguous=False)
-    _tensor(v, "v", (B, Hkv, dv), ty, dev, contiguous=False)
-    _heads_row(q, "q")
-    _heads_row(k, "k")
-    _heads_row(v, "v")
-    _tensor(k_cache, "k_cache", (B, window + sinks, Hkv, dk), ty, dev)
-    _tensor(v_cache, "v_cache", (B, window + sinks, Hkv, dv), ty, dev)
-    _tensor(pos, "pos", (B,), torch.int32, dev)
-    out = _new(out, "out", (B, Hq, dv), ty, dev, None)
-    _call("gdn_window_attention_step", dev, q.data_ptr(), q.stride(0), k.data_ptr(), k.stride(0), v.data_ptr(),
-          v.stride(0), k_cache.data_ptr(), v_cache.data_ptr(), pos.data_ptr(), out.data_ptr(), B, Hq, Hkv, dk, dv,
-          window, sinks, dk ** -0.5 if scale is None else scale)
+    _, Hkv, dv = v.shape
+    qp, qs = _token(q, "q", q.shape, ty, dev)
+    kp, ks = _token(k, "k", (B, Hkv, dk), ty, dev)
+    vp, vs = _token(v, "v", (B, Hkv, dv), ty, dev)
+    kc = _whole(k_cache, "k_cache", (B, window + sinks, Hkv, dk), ty, dev)
+    vc = _whole(v_cache, "v_cache", (B, window + sinks, Hkv, dv), ty, dev)
+    pp = _whole(pos, "pos", (B,), i32, dev)
+    out = _new(out, "out", q, (B, Hq, dv), ty)
+    _call("gdn_window_attention_step", dev, qp, qs[0], kp, ks[0], vp, vs[0], kc, vc, pp, out.data_ptr(), B, Hq, Hkv, dk,
+          dv, window, sinks, dk ** -0.5 if scale is None else scale)
     return out

@@ -512,13 +512,16 @@ def test_captured_and_replayed_beside_eager_calls(cuda):
 
 @pytest.mark.parametrize("step", [False, True])
 def test_window_attention_timeout_is_reported_and_recovers(cuda, step):
-    """A wait that runs out (the bound shortened to 1 ns) is reported, and the next call is right."""
+    """A wait that runs out (the bound shortened to 1 ns) is reported, and the next call is right.
+
+    A wait that finds its copy there gives nothing to report, so the step reads 512 MB from all SMs at
+    once: HBM keeps its warps waiting."""
     g = gen(12)
     if step:
-        q, k, v = attn_inputs(g, 2, 1, 1, 8, 2, 112, 112)
-        kc, vc = normal(g, 2, 2010, 2, 112, dtype=torch.bfloat16), normal(g, 2, 2010, 2, 112, dtype=torch.bfloat16)
-        pos = torch.tensor([5000, 1700], dtype=torch.int32, device=cuda)
-        call = lambda: G.window_attention_step(q[:, 0], k[:, 0], v[:, 0], kc, vc, pos, 2000, 10)
+        q, k, v = attn_inputs(g, 32, 1, 1, 8, 8, 128, 128)
+        kc, vc = (normal(g, 32, 4010, 8, 128, dtype=torch.bfloat16) for _ in range(2))
+        pos = torch.full((32,), 5000, dtype=torch.int32, device=cuda)
+        call = lambda: G.window_attention_step(q[:, 0], k[:, 0], v[:, 0], kc, vc, pos, 4000, 10)
     else:
         q, k, v = attn_inputs(g, 1, 2000, 2000, 4, 2, 112, 112)
         call = lambda: G.window_attention(q, k, v, 500, 20)
