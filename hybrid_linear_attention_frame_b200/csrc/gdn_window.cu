@@ -69,9 +69,10 @@ bool make_map(CUtensorMap* map, const void* ptr, int d, int H, long long T, int 
 // One CTA per pair of 128-query tiles (two query heads that share a key head where there are
 // such, else two tiles of consecutive queries), which read the same K and V tiles:
 //   S_q = Q_q K^T on the tensor cores into TMEM, q = 0, 1;
-//   softmax of tile q by its own four warps, one thread per query row, against a lazily moved
-//     reference maximum m (it moves only when a score exceeds it by more than 2^8, so O is
-//     rarely rescaled; the division by the running sum at the end is exact for any m);
+//   softmax of tile q by its own four warps, one thread per query row, against a reference m, the
+//     row's largest score in its first tile: it moves only when a tile's weights sum to more than
+//     2^30, so later tiles need no maximum and O is hardly ever rescaled (the division by the
+//     running sum at the end is right for any m);
 //   P in bf16 over the score columns it came from, O_q += P_q V with P as the A operand.
 // Warp 8 issues the MMAs in the order PV_0(j-1) S_0(j) PV_1(j-1) S_1(j), so that the tensor
 // cores work for one tile while the other's softmax runs; they execute in order, so S_q(j)
@@ -106,7 +107,7 @@ constexpr uint32_t kSmemBytes = kOffTmemSlot + 16u + 1024u;      // + slack for 
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;     // + 128 q each
-constexpr float kMoveRef = 8.0f;               // log2 units
+constexpr float kMaxSum = 1073741824.0f;       // of a row's weights in a tile, before its reference moves
 constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
 
 struct Args {
@@ -119,7 +120,7 @@ struct Args {
     uint64_t wait_limit_ns;
 };
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
     uint32_t r[32];
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32"
                  " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -134,18 +135,29 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// Waits for this thread's TMEM loads; x is what they bring (nothing that uses it moves before the wait).
+__device__ __forceinline__ void tmem_wait32(float (&x)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7]),
+                   "+f"(x[8]), "+f"(x[9]), "+f"(x[10]), "+f"(x[11]), "+f"(x[12]), "+f"(x[13]), "+f"(x[14]),
+                   "+f"(x[15]), "+f"(x[16]), "+f"(x[17]), "+f"(x[18]), "+f"(x[19]), "+f"(x[20]), "+f"(x[21]),
+                   "+f"(x[22]), "+f"(x[23]), "+f"(x[24]), "+f"(x[25]), "+f"(x[26]), "+f"(x[27]), "+f"(x[28]),
+                   "+f"(x[29]), "+f"(x[30]), "+f"(x[31])
+                 :: "memory");
+}
+
+// the n lowest bits, none below 0, all above 31
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
 // What a CTA visits: its two query tiles' rows and the key tiles of their union.
 struct Plan {
     int head[2], row0[2];                      // query head and first query of tile q
     int p_lo[2], p_hi[2];                      // positions of its first and last live query; none if p_hi < p_lo
     int sink, startB, nA, n;                   // sink tiles 0 .. nA-1, then tiles from startB on
+    // tile q sees keys of tiles 0 .. first_end - 1 (sinks) and near .. end - 1 (its window)
+    int first_end[2], near[2], end[2];
     __device__ int start(int j) const { return j < nA ? kBN * j : startB + kBN * (j - nA); }
-    // does query tile q see a key of tile j?
-    __device__ bool active(int lo, int hi, int j, int window) const {
-        const int s0 = start(j);
-        return hi >= lo && s0 <= hi && (s0 < sink || s0 + kBN > lo - window + 1);
-    }
-    __device__ bool active(int q, int j, int window) const { return active(p_lo[q], p_hi[q], j, window); }
+    __device__ bool active(int q, int j) const { return j < first_end[q] || (j >= near[q] && j < end[q]); }
 };
 
 __device__ __forceinline__ Plan make_plan(const Args& a, int n_keys) {
@@ -172,14 +184,18 @@ __device__ __forceinline__ Plan make_plan(const Args& a, int n_keys) {
     p.nA = split ? (p.sink + kBN - 1) / kBN : 0;
     p.startB = split ? w_lo : 0;
     p.n = hi < 0 ? 0 : p.nA + (hi + 1 - p.startB + kBN - 1) / kBN;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const bool live = p.p_hi[q] >= p.p_lo[q];
+        const int w = max(0, p.p_lo[q] - a.window + 1);
+        p.end[q] = live ? p.nA + (p.p_hi[q] - p.startB) / kBN + 1 : 0;
+        p.near[q] = live ? p.nA + (w - p.startB) / kBN : 0;
+        p.first_end[q] = live ? min(split ? p.nA : (p.sink + kBN - 1) / kBN, p.end[q]) : 0;
+    }
     return p;
 }
 
 __device__ __forceinline__ uint64_t kmaj(uint32_t addr) { return smem_desc(addr, 16, 1024, kSwizzle128); }
-__device__ __forceinline__ uint32_t kstep(uint32_t op, int ks) {
-    return op + (ks >= 4 ? kBox : 0u) + (uint32_t)(ks & 3) * 32u;
-}
-
 __global__ void __launch_bounds__(kThreads, 1)
 window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const Args a)
@@ -262,48 +278,51 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(i), parity & 1u, abort_flag, lim, code));
             return ok;
         };
-        int steps[2] = {0, 0};                 // key tiles whose P V was issued
+        uint32_t steps[2] = {0, 0};            // key tiles whose P V was issued
         wait(kBarQ, 0, 43);
+#pragma unroll 1
         for (int j = 0; ok && j <= p.n; ++j) {
-            const bool last_v = j >= 1 && p.active(1, j - 1, a.window);      // tile 1 is V's last reader
-            const bool last_k = j < p.n && p.active(1, j, a.window);
+            const bool pv[2] = {j >= 1 && p.active(0, j - 1), j >= 1 && p.active(1, j - 1)};
+            const bool qk[2] = {j < p.n && p.active(0, j), j < p.n && p.active(1, j)};
+            const int sv = (j - 1) % kVStages, sk = j % kKStages;
+            const uint32_t v = base + kOffV + (uint32_t)max(sv, 0) * kOp, ko = base + kOffK + sk * kOp;
+            const uint64_t vdesc = smem_desc(v, kBox, 1024, kSwizzle128), kdesc = kmaj(ko);
+            if (j >= 1) {
+                if (!wait(kBarVFull + sv, (uint32_t)((j - 1) / kVStages), 44)) break;
+                // rows of padding in V hold anything: zero times that must be zero
+                const int live = n_keys - p.start(j - 1);
+                if (live < kBN && n_keys < a.Tk) {
+                    for (int r = live * 8 + lane; r < kBN * 8; r += 32)
+                        for (int c = 0; c < nbv; ++c) st_shared_v4(v + c * kBox + 16u * r, 0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+            }
+            if (j < p.n && !wait(kBarKFull + sk, (uint32_t)(j / kKStages), 46)) break;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                if (j >= 1 && p.active(q, j - 1, a.window)) {
-                    const int sv = (j - 1) % kVStages;
-                    const uint32_t v = base + kOffV + sv * kOp;
-                    if (!wait(kBarVFull + sv, (uint32_t)((j - 1) / kVStages), 44)) break;
-                    // rows of padding in V hold anything: zero times that must be zero
-                    const int live = n_keys - p.start(j - 1);
-                    if (live < kBN && n_keys < a.Tk && (q == 0 || !p.active(0, j - 1, a.window))) {
-                        for (int r = live * 8 + lane; r < kBN * 8; r += 32)
-                            for (int c = 0; c < nbv; ++c) st_shared_v4(v + c * kBox + 16u * r, 0, 0, 0, 0);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    if (!wait(kBarP + q, (uint32_t)steps[q], 45)) break;
+                if (pv[q]) {
+                    if (!wait(kBarP + q, steps[q], 45)) break;
                     tc_fence_after();
+                    // a K step of 16 keys: 8 columns of P, 2048 bytes (128 descriptor units) of V
 #pragma unroll
                     for (int ks = 0; ks < kBN / 16; ++ks)
                         attn::mma_bf16_tmem_a_warp(tmem + kColO + 128u * q, tmem + kColS + 128u * q + 8u * ks,
-                                                   smem_desc(v + (uint32_t)ks * 2048u, kBox, 1024, kSwizzle128), idpv,
-                                                   (steps[q] > 0 || ks > 0) ? 1u : 0u);
+                                                   vdesc + 128u * ks, idpv, (steps[q] > 0 || ks > 0) ? 1u : 0u);
                     ++steps[q];
-                    if (q == 1 || !last_v) mma_commit_warp(bar(kBarVFree + sv));
-                    bool more = false;
-                    for (int jj = j; jj < p.n && !more; ++jj) more = p.active(q, jj, a.window);
-                    if (!more) mma_commit_warp(bar(kBarO + q));
+                    if (q == 1 || !pv[1]) mma_commit_warp(bar(kBarVFree + sv));
+                    if (j == p.end[q]) mma_commit_warp(bar(kBarO + q));
                 }
-                if (j < p.n && p.active(q, j, a.window)) {
-                    const int sk = j % kKStages;
-                    if (!wait(kBarKFull + sk, (uint32_t)(j / kKStages), 46)) break;
-                    tc_fence_after();
-                    const uint32_t qo = base + kOffQ + q * kOp, ko = base + kOffK + sk * kOp;
-#pragma unroll 1
-                    for (int ks = 0; ks < nks; ++ks)
-                        mma_bf16_warp(tmem + kColS + 128u * q, kmaj(kstep(qo, ks)), kmaj(kstep(ko, ks)), kIdS, ks > 0);
+                if (qk[q]) {
+                    const uint64_t qdesc = kmaj(base + kOffQ + q * kOp);
+                    // a K step of 16 head elements: 32 bytes inside a box, four of them per box
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        if (ks < nks)
+                            mma_bf16_warp(tmem + kColS + 128u * q, qdesc + (ks >> 2) * (kBox >> 4) + 2u * (ks & 3),
+                                          kdesc + (ks >> 2) * (kBox >> 4) + 2u * (ks & 3), kIdS, ks > 0);
                     mma_commit_warp(bar(kBarS + q));
-                    if (q == 1 || !last_k) mma_commit_warp(bar(kBarKFree + sk));
+                    if (q == 1 || !qk[1]) mma_commit_warp(bar(kBarKFree + sk));
                 }
             }
         }
@@ -316,6 +335,8 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int q = warp >> 2;
         const int p_lo = q ? p.p_lo[1] : p.p_lo[0], p_hi = q ? p.p_hi[1] : p.p_hi[0];
         const int row0 = q ? p.row0[1] : p.row0[0], head = q ? p.head[1] : p.head[0];
+        const int first_end = q ? p.first_end[1] : p.first_end[0], near = q ? p.near[1] : p.near[0];
+        const int end = q ? p.end[1] : p.end[0];
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ts = lane_base + kColS + 128u * q, to = lane_base + kColO + 128u * q;
         const int row = (warp & 3) * 32 + lane;
@@ -326,67 +347,104 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         bool ok = true;
         int i = 0;                                            // key tiles taken
         for (int j = 0; j < p.n; ++j) {
-            if (!p.active(p_lo, p_hi, j, a.window)) continue;
+            if (!(j < first_end || (j >= near && j < end))) continue;
             ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarS + q), (uint32_t)(i & 1), abort_flag, lim, 47));
             if (!ok) break;
             tc_fence_after();
-            float x[kBN];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32u * c, x + 32 * c);
             const int s0 = p.start(j);
             const bool sink_tile = j < p.nA;
             // columns [lo, hi] are in the row's window, columns below sk among the sinks
             const int hi = sink_tile ? -1 : min(t, n_keys - 1) - s0;
             const int lo = ws - s0, sk = (split && !sink_tile) ? 0 : min(p.sink, t + 1) - s0;
-            const bool full = (lo <= 0 && hi >= kBN - 1) || sk >= kBN;
-            tmem_wait_ld();
-            if (__any_sync(0xffffffffu, !full)) {
+            const bool masked = __any_sync(0xffffffffu, !((lo <= 0 && hi >= kBN - 1) || sk >= kBN));
+            auto mask = [&](float (&x)[32], int c) {
+                if (masked) {
+                    const uint32_t keep = (low_bits(hi + 1 - 32 * c) & ~low_bits(lo - 32 * c)) | low_bits(sk - 32 * c);
 #pragma unroll
-                for (int e = 0; e < kBN; ++e) x[e] = ((e >= lo && e <= hi) || e < sk) ? x[e] : -INFINITY;
-            }
-            float mx[4] = {x[0], x[1], x[2], x[3]};
+                    for (int e = 0; e < 32; ++e) x[e] = (keep & (1u << e)) ? x[e] : -INFINITY;
+                }
+            };
+            // 2^(x scale - m) of the whole row, without looking for its maximum first: m is a score of an
+            // earlier tile, and float and bf16 hold what is 2^30 times as large as well as what is as
+            // large.  Rows without a reference yet, or with a sum beyond that, take the long way.
+            uint32_t pk[kBN / 2];
+            float sum;
+            bool look = __any_sync(0xffffffffu, m_ref == -INFINITY);
+            while (true) {
+                float xa[32], xb[32];
+                if (look) {
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    auto top = [&](float (&x)[32], int c) {
+                        mask(x, c);
 #pragma unroll
-            for (int e = 0; e < (kBN - 4) / 2; ++e) mx[e & 3] = attn::max3f(mx[e & 3], x[4 + 2 * e], x[5 + 2 * e]);
-            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-            const bool move = mt > m_ref + kMoveRef;
-            float alpha = 1.0f;
-            if (move) {
-                alpha = attn::ex2(m_ref - mt);
-                m_ref = mt;
-            }
-            // O is rescaled where a row of the warp moved (TMEM accesses are warp-collective); its
-            // last P V is done, since the scores that followed it are here
-            if (i > 0 && __any_sync(0xffffffffu, move)) {
+                        for (int e = 0; e < 16; ++e) mx[e & 3] = attn::max3f(mx[e & 3], x[2 * e], x[2 * e + 1]);
+                    };
+                    tmem_ld32(ts, xa);
+                    tmem_wait32(xa);
+                    tmem_ld32(ts + 32, xb);
+                    top(xa, 0);
+                    tmem_wait32(xb);
+                    tmem_ld32(ts + 64, xa);
+                    top(xb, 1);
+                    tmem_wait32(xa);
+                    tmem_ld32(ts + 96, xb);
+                    top(xa, 2);
+                    tmem_wait32(xb);
+                    top(xb, 3);
+                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+                    const float mn = fmaxf(m_ref, mt);
+                    const float alpha = mn > m_ref ? attn::ex2(m_ref - mn) : 1.0f;
+                    l *= alpha;
+                    m_ref = mn;
+                    // (TMEM accesses are warp-collective: the other rows' alpha is 1)
+                    if (i > 0) {
 #pragma unroll 1
-                for (int c = 0; c < a.dv / 16; ++c) {
-                    float o[16];
-                    tmem_ld16(to + 16u * c, o);
-                    tmem_wait_ld();
+                        for (int c = 0; c < a.dv / 16; ++c) {
+                            float o[16];
+                            tmem_ld16(to + 16u * c, o);
+                            tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] *= alpha;
-                    attn::tmem_st16(to + 16u * c, o);
+                            for (int e = 0; e < 16; ++e) o[e] *= alpha;
+                            attn::tmem_st16(to + 16u * c, o);
+                        }
+                    }
                 }
+                const float neg_mr = (m_ref == -INFINITY) ? 0.0f : -m_ref;
+                const uint64_t sc2 = attn::f2pack(a.scale_log2, a.scale_log2), nm2 = attn::f2pack(neg_mr, neg_mr);
+                uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+                auto weigh = [&](float (&x)[32], int c) {
+                    mask(x, c);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float t0, t1;
+                        attn::f2unpack(attn::fma2(attn::f2pack(x[2 * e], x[2 * e + 1]), sc2, nm2), t0, t1);
+                        const float p0 = attn::ex2(t0), p1 = attn::ex2(t1);
+                        acc[e & 3] = attn::add2(acc[e & 3], attn::f2pack(p0, p1));
+                        pk[16 * c + e] = pack_bf16x2(p0, p1);
+                    }
+                };
+                tmem_ld32(ts, xa);
+                tmem_wait32(xa);
+                tmem_ld32(ts + 32, xb);            // in flight while the 32 before are worked on
+                weigh(xa, 0);
+                tmem_wait32(xb);
+                tmem_ld32(ts + 64, xa);
+                weigh(xb, 1);
+                tmem_wait32(xa);
+                tmem_ld32(ts + 96, xb);
+                weigh(xa, 2);
+                tmem_wait32(xb);
+                weigh(xb, 3);
+                float sm[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) attn::f2unpack(acc[e], sm[2 * e], sm[2 * e + 1]);
+                sum = ((sm[0] + sm[1]) + (sm[2] + sm[3])) + ((sm[4] + sm[5]) + (sm[6] + sm[7]));
+                if (look || !__any_sync(0xffffffffu, !(sum <= kMaxSum))) break;
+                look = true;
             }
-            const float neg_mr = (m_ref == -INFINITY) ? 0.0f : -m_ref;
-            const uint64_t sc2 = attn::f2pack(a.scale_log2, a.scale_log2), nm2 = attn::f2pack(neg_mr, neg_mr);
-            uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+            l += sum;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float t0, t1;
-                    attn::f2unpack(attn::fma2(attn::f2pack(x[32 * c + 2 * e], x[32 * c + 2 * e + 1]), sc2, nm2), t0, t1);
-                    const float p0 = attn::ex2(t0), p1 = attn::ex2(t1);
-                    acc[e & 3] = attn::add2(acc[e & 3], attn::f2pack(p0, p1));
-                    pk[e] = pack_bf16x2(p0, p1);
-                }
-                attn::tmem_st16u(ts + 16u * c, pk);
-            }
-            float sm[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) attn::f2unpack(acc[e], sm[2 * e], sm[2 * e + 1]);
-            l = l * alpha + (((sm[0] + sm[1]) + (sm[2] + sm[3])) + ((sm[4] + sm[5]) + (sm[6] + sm[7])));
+            for (int c = 0; c < 4; ++c) attn::tmem_st16u(ts + 16u * c, pk + 16 * c);
             attn::tmem_wait_st();
             tc_fence_before();
             __syncwarp();
