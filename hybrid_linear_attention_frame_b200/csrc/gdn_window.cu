@@ -97,8 +97,9 @@ constexpr uint32_t kOffV = kOffK + kKStages * kOp;
 constexpr uint32_t kOffBar = kOffV + kVStages * kOp;
 enum : uint32_t { kBarQ = 0, kBarKFull = 1, kBarKFree = kBarKFull + kKStages, kBarVFull = kBarKFree + kKStages,
                   kBarVFree = kBarVFull + kVStages, kBarS = kBarVFree + kVStages,   // [2] scores ready
-                  kBarP = kBarS + 2,           // [2] P written, O rescaled (one arrival per softmax warp)
-                  kBarO = kBarP + 2,           // [2] last PV of the tile done
+                  kBarP = kBarS + 2,           // [2][2] half of P written, O rescaled (an arrival per softmax warp)
+                  kBarH = kBarP + 4,           // [2] P V of a step's first half done
+                  kBarO = kBarH + 2,           // [2] last P V of the tile done
                   kBarDrain = kBarO + 2,       // every MMA done
                   kNumBars = kBarDrain + 1 };
 constexpr uint32_t kOffAbort = kOffBar + 8u * kNumBars;
@@ -144,6 +145,28 @@ __device__ __forceinline__ void tmem_wait32(float (&x)[32]) {
                    "+f"(x[22]), "+f"(x[23]), "+f"(x[24]), "+f"(x[25]), "+f"(x[26]), "+f"(x[27]), "+f"(x[28]),
                    "+f"(x[29]), "+f"(x[30]), "+f"(x[31])
                  :: "memory");
+}
+
+constexpr float kE0 = 9.99928073e-01f, kE1 = 6.93260985e-01f, kE2 = 2.42611125e-01f, kE3 = 5.51716703e-02f;
+
+// 2^y of a pair on the FMA pipe: y = r + f with r whole (adding 1.5 2^23 rounds to it), f in
+// [-1/2, 1/2], 2^f by the cubic that is least off in relative error there (1e-4, a twentieth of the
+// weight's rounding to bf16), r added to the exponent.  y is held in [-126, 127]: far below, the
+// weight is as good as 0; far above, the sum shows it.
+__device__ __forceinline__ void ex2_fma(uint64_t y, float& p0, float& p1) {
+    float y0, y1, r0, r1;
+    attn::f2unpack(y, y0, y1);
+    const uint64_t c = attn::f2pack(fminf(fmaxf(y0, -126.0f), 127.0f), fminf(fmaxf(y1, -126.0f), 127.0f));
+    const uint64_t magic = attn::f2pack(12582912.0f, 12582912.0f), back = attn::f2pack(-12582912.0f, -12582912.0f);
+    const uint64_t r = attn::add2(c, magic);
+    const uint64_t f = attn::fma2(attn::add2(r, back), attn::f2pack(-1.0f, -1.0f), c);
+    uint64_t v = attn::fma2(f, attn::f2pack(kE3, kE3), attn::f2pack(kE2, kE2));
+    v = attn::fma2(v, f, attn::f2pack(kE1, kE1));
+    v = attn::fma2(v, f, attn::f2pack(kE0, kE0));
+    attn::f2unpack(r, r0, r1);
+    attn::f2unpack(v, p0, p1);
+    p0 = __int_as_float(__float_as_int(p0) + (__float_as_int(r0) << 23));
+    p1 = __int_as_float(__float_as_int(p1) + (__float_as_int(r1) << 23));
 }
 
 // the n lowest bits, none below 0, all above 31
@@ -196,6 +219,16 @@ __device__ __forceinline__ Plan make_plan(const Args& a, int n_keys) {
 }
 
 __device__ __forceinline__ uint64_t kmaj(uint32_t addr) { return smem_desc(addr, 16, 1024, kSwizzle128); }
+// One MMA of the calling thread whose A operand is in TMEM (row m in lane m, a bf16 pair per column).
+__device__ __forceinline__ void mma_bf16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                                uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 :: "r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
 window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const Args a)
@@ -219,7 +252,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tmem_relinquish();
     }
     if (tid == 32) {
-        for (uint32_t i = 0; i < kNumBars; ++i) mbar_init(bar(i), (i >= kBarP && i < kBarP + 2) ? 4u : 1u);
+        for (uint32_t i = 0; i < kNumBars; ++i) mbar_init(bar(i), (i >= kBarP && i < kBarP + 4) ? 4u : 1u);
         fence_mbar_init();
         *abort_flag = 0;
         tma_prefetch_desc(&tm_q);
@@ -270,65 +303,63 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
-        // ======================= MMAs =======================
-        const int nks = a.dk / 16;
-        const uint32_t idpv = idesc_bf16(128, a.dv, false, true);
-        bool ok = true;
-        auto wait = [&](uint32_t i, uint32_t parity, int code) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(i), parity & 1u, abort_flag, lim, code));
-            return ok;
-        };
-        uint32_t steps[2] = {0, 0};            // key tiles whose P V was issued
-        wait(kBarQ, 0, 43);
+        // ======================= MMAs (one thread issues them all) =======================
+        if (elect_one()) {
+            const int nks = a.dk / 16;
+            const uint32_t idpv = idesc_bf16(128, a.dv, false, true);
+            const uint64_t q0desc = kmaj(base + kOffQ), k0desc = kmaj(base + kOffK);
+            const uint64_t v0desc = smem_desc(base + kOffV, kBox, 1024, kSwizzle128);
+            uint32_t sk = 0, pk = 0, sv = 0, pv = 0;       // stage and phase of K(j) and of V(j - 1)
+            uint32_t steps[2] = {0, 0};                    // key tiles whose P V was issued
+            bool ok = mbar_wait(bar(kBarQ), 0, abort_flag, lim, 43);
 #pragma unroll 1
-        for (int j = 0; ok && j <= p.n; ++j) {
-            const bool pv[2] = {j >= 1 && p.active(0, j - 1), j >= 1 && p.active(1, j - 1)};
-            const bool qk[2] = {j < p.n && p.active(0, j), j < p.n && p.active(1, j)};
-            const int sv = (j - 1) % kVStages, sk = j % kKStages;
-            const uint32_t v = base + kOffV + (uint32_t)max(sv, 0) * kOp, ko = base + kOffK + sk * kOp;
-            const uint64_t vdesc = smem_desc(v, kBox, 1024, kSwizzle128), kdesc = kmaj(ko);
-            if (j >= 1) {
-                if (!wait(kBarVFull + sv, (uint32_t)((j - 1) / kVStages), 44)) break;
-                // rows of padding in V hold anything: zero times that must be zero
-                const int live = n_keys - p.start(j - 1);
-                if (live < kBN && n_keys < a.Tk) {
-                    for (int r = live * 8 + lane; r < kBN * 8; r += 32)
-                        for (int c = 0; c < nbv; ++c) st_shared_v4(v + c * kBox + 16u * r, 0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
+            for (int j = 0; ok && j <= p.n; ++j) {
+                const bool dopv[2] = {j >= 1 && p.active(0, j - 1), j >= 1 && p.active(1, j - 1)};
+                const bool doqk[2] = {j < p.n && p.active(0, j), j < p.n && p.active(1, j)};
+                if (j >= 1) ok = mbar_wait(bar(kBarVFull + sv), pv, abort_flag, lim, 44);
+                if (j < p.n) ok = ok && mbar_wait(bar(kBarKFull + sk), pk, abort_flag, lim, 46);
+                if (!ok) break;
+                const uint64_t vdesc = v0desc + sv * (kOp >> 4), kdesc = k0desc + sk * (kOp >> 4);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    if (dopv[q]) {
+                        // a K step of 16 keys: 8 columns of P (whose halves lie 64 columns apart), 2048 bytes
+                        // (128 descriptor units) of V
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            ok = ok && mbar_wait(bar(kBarP + 2 * q + h), steps[q] & 1u, abort_flag, lim, 45);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int ks = 0; ks < kBN / 32; ++ks)
+                                mma_bf16_tmem_a(tmem + kColO + 128u * q, tmem + kColS + 128u * q + 64u * h + 8u * ks,
+                                                vdesc + 128u * (4 * h + ks), idpv, (steps[q] > 0 || h + ks > 0) ? 1u : 0u);
+                            if (h == 0) mma_commit(bar(kBarH + q));
+                        }
+                        if (!ok) break;
+                        ++steps[q];
+                        if (q == 1 || !dopv[1]) mma_commit(bar(kBarVFree + sv));
+                        if (j == p.end[q]) mma_commit(bar(kBarO + q));
+                    }
+                    if (doqk[q]) {
+                        const uint64_t qdesc = q0desc + q * (kOp >> 4);
+                        // a K step of 16 head elements: 32 bytes inside a box, four of them per box
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            if (ks < nks)
+                                mma_bf16(tmem + kColS + 128u * q, qdesc + (ks >> 2) * (kBox >> 4) + 2u * (ks & 3),
+                                         kdesc + (ks >> 2) * (kBox >> 4) + 2u * (ks & 3), kIdS, ks > 0);
+                        mma_commit(bar(kBarS + q));
+                        if (q == 1 || !doqk[1]) mma_commit(bar(kBarKFree + sk));
+                    }
                 }
+                if (j >= 1 && ++sv == kVStages) { sv = 0; pv ^= 1u; }
+                if (++sk == kKStages) { sk = 0; pk ^= 1u; }
             }
-            if (j < p.n && !wait(kBarKFull + sk, (uint32_t)(j / kKStages), 46)) break;
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                if (pv[q]) {
-                    if (!wait(kBarP + q, steps[q], 45)) break;
-                    tc_fence_after();
-                    // a K step of 16 keys: 8 columns of P, 2048 bytes (128 descriptor units) of V
-#pragma unroll
-                    for (int ks = 0; ks < kBN / 16; ++ks)
-                        attn::mma_bf16_tmem_a_warp(tmem + kColO + 128u * q, tmem + kColS + 128u * q + 8u * ks,
-                                                   vdesc + 128u * ks, idpv, (steps[q] > 0 || ks > 0) ? 1u : 0u);
-                    ++steps[q];
-                    if (q == 1 || !pv[1]) mma_commit_warp(bar(kBarVFree + sv));
-                    if (j == p.end[q]) mma_commit_warp(bar(kBarO + q));
-                }
-                if (qk[q]) {
-                    const uint64_t qdesc = kmaj(base + kOffQ + q * kOp);
-                    // a K step of 16 head elements: 32 bytes inside a box, four of them per box
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        if (ks < nks)
-                            mma_bf16_warp(tmem + kColS + 128u * q, qdesc + (ks >> 2) * (kBox >> 4) + 2u * (ks & 3),
-                                          kdesc + (ks >> 2) * (kBox >> 4) + 2u * (ks & 3), kIdS, ks > 0);
-                    mma_commit_warp(bar(kBarS + q));
-                    if (q == 1 || !qk[1]) mma_commit_warp(bar(kBarKFree + sk));
-                }
-            }
+            // every MMA is done before shared memory and TMEM go away, whoever gave up
+            mma_commit(bar(kBarDrain));
+            drain_wait(bar(kBarDrain), 0);
         }
-        // every MMA is done before shared memory and TMEM go away, whoever gave up
-        mma_commit_warp(bar(kBarDrain));
-        if (lane == 0) drain_wait(bar(kBarDrain), 0);
         __syncwarp();
     } else {
         // ======================= softmax of tile q, one thread per row =======================
@@ -348,9 +379,6 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         int i = 0;                                            // key tiles taken
         for (int j = 0; j < p.n; ++j) {
             if (!(j < first_end || (j >= near && j < end))) continue;
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarS + q), (uint32_t)(i & 1), abort_flag, lim, 47));
-            if (!ok) break;
-            tc_fence_after();
             const int s0 = p.start(j);
             const bool sink_tile = j < p.nA;
             // columns [lo, hi] are in the row's window, columns below sk among the sinks
@@ -364,91 +392,111 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     for (int e = 0; e < 32; ++e) x[e] = (keep & (1u << e)) ? x[e] : -INFINITY;
                 }
             };
-            // 2^(x scale - m) of the whole row, without looking for its maximum first: m is a score of an
-            // earlier tile, and float and bf16 hold what is 2^30 times as large as well as what is as
-            // large.  Rows without a reference yet, or with a sum beyond that, take the long way.
-            uint32_t pk[kBN / 2];
-            float sum;
-            bool look = __any_sync(0xffffffffu, m_ref == -INFINITY);
-            while (true) {
-                float xa[32], xb[32];
-                if (look) {
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    auto top = [&](float (&x)[32], int c) {
-                        mask(x, c);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) mx[e & 3] = attn::max3f(mx[e & 3], x[2 * e], x[2 * e + 1]);
-                    };
-                    tmem_ld32(ts, xa);
-                    tmem_wait32(xa);
-                    tmem_ld32(ts + 32, xb);
-                    top(xa, 0);
-                    tmem_wait32(xb);
-                    tmem_ld32(ts + 64, xa);
-                    top(xb, 1);
-                    tmem_wait32(xa);
-                    tmem_ld32(ts + 96, xb);
-                    top(xa, 2);
-                    tmem_wait32(xb);
-                    top(xb, 3);
-                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-                    const float mn = fmaxf(m_ref, mt);
-                    const float alpha = mn > m_ref ? attn::ex2(m_ref - mn) : 1.0f;
-                    l *= alpha;
-                    m_ref = mn;
-                    // (TMEM accesses are warp-collective: the other rows' alpha is 1)
-                    if (i > 0) {
+            // rows of padding in V hold anything: zero times that must be zero
+            if (n_keys - s0 < kBN && n_keys < a.Tk) {
+                const uint32_t v = base + kOffV + (uint32_t)(j % kVStages) * kOp;
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarVFull + j % kVStages), (uint32_t)(j / kVStages) & 1u,
+                                                       abort_flag, lim, 49));
+                if (!ok) break;
+                for (int r = (n_keys - s0) * 8 + row; r < kBN * 8; r += kBM)
+                    for (int c = 0; c < nbv; ++c) st_shared_v4(v + c * kBox + 16u * r, 0, 0, 0, 0);
+                fence_proxy_async_smem();
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarS + q), (uint32_t)(i & 1), abort_flag, lim, 47));
+            if (!ok) break;
+            tc_fence_after();
+            float xa[32], xb[32];
+            // Moves the references up to the rows' largest scores among columns 32 c0 .. 127 (O is
+            // complete up to here: the P V issued so far are done).
+            auto look_up = [&](int c0) {
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                        for (int c = 0; c < a.dv / 16; ++c) {
-                            float o[16];
-                            tmem_ld16(to + 16u * c, o);
-                            tmem_wait_ld();
+                for (int c = c0; c < 4; ++c) {
+                    tmem_ld32(ts + 32u * c, xa);
+                    tmem_wait32(xa);
+                    mask(xa, c);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] *= alpha;
-                            attn::tmem_st16(to + 16u * c, o);
-                        }
+                    for (int e = 0; e < 16; ++e) mx[e & 3] = attn::max3f(mx[e & 3], xa[2 * e], xa[2 * e + 1]);
+                }
+                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+                const float mn = fmaxf(m_ref, mt);
+                const float alpha = mn > m_ref ? attn::ex2(m_ref - mn) : 1.0f;
+                l *= alpha;
+                m_ref = mn;
+                // (TMEM accesses are warp-collective: the other rows' alpha is 1)
+                if (i > 0 || c0 > 0) {
+#pragma unroll 1
+                    for (int c = 0; c < a.dv / 16; ++c) {
+                        float o[16];
+                        tmem_ld16(to + 16u * c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] *= alpha;
+                        attn::tmem_st16(to + 16u * c, o);
                     }
                 }
-                const float neg_mr = (m_ref == -INFINITY) ? 0.0f : -m_ref;
-                const uint64_t sc2 = attn::f2pack(a.scale_log2, a.scale_log2), nm2 = attn::f2pack(neg_mr, neg_mr);
-                uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-                auto weigh = [&](float (&x)[32], int c) {
-                    mask(x, c);
+            };
+            if (__any_sync(0xffffffffu, m_ref == -INFINITY)) look_up(0);
+            // 2^(x scale - m) without looking for the maximum first: m is a score of an earlier tile, and
+            // float and bf16 hold what is 2^30 times as large as well as what is as large.  Half by half,
+            // so that P V of the first runs beside the second.
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                uint32_t pk[32];
+                float sum;
+                bool again = false;
+                while (true) {
+                    const float neg_mr = (m_ref == -INFINITY) ? 0.0f : -m_ref;
+                    const uint64_t sc2 = attn::f2pack(a.scale_log2, a.scale_log2), nm2 = attn::f2pack(neg_mr, neg_mr);
+                    uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+                    auto weigh = [&](float (&x)[32], int c) {
+                        mask(x, 2 * h + c);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float t0, t1;
-                        attn::f2unpack(attn::fma2(attn::f2pack(x[2 * e], x[2 * e + 1]), sc2, nm2), t0, t1);
-                        const float p0 = attn::ex2(t0), p1 = attn::ex2(t1);
-                        acc[e & 3] = attn::add2(acc[e & 3], attn::f2pack(p0, p1));
-                        pk[16 * c + e] = pack_bf16x2(p0, p1);
+                        for (int e = 0; e < 16; ++e) {
+                            const uint64_t y = attn::fma2(attn::f2pack(x[2 * e], x[2 * e + 1]), sc2, nm2);
+                            float p0, p1;
+                            if (e % 8 == 7) {
+                                ex2_fma(y, p0, p1);
+                            } else {
+                                attn::f2unpack(y, p0, p1);
+                                p0 = attn::ex2(p0);
+                                p1 = attn::ex2(p1);
+                            }
+                            acc[e & 3] = attn::add2(acc[e & 3], attn::f2pack(p0, p1));
+                            pk[16 * c + e] = pack_bf16x2(p0, p1);
+                        }
+                    };
+                    tmem_ld32(ts + 64u * h, xa);
+                    tmem_wait32(xa);
+                    tmem_ld32(ts + 64u * h + 32, xb);      // in flight while the 32 before are worked on
+                    weigh(xa, 0);
+                    tmem_wait32(xb);
+                    weigh(xb, 1);
+                    float sm[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) attn::f2unpack(acc[e], sm[2 * e], sm[2 * e + 1]);
+                    sum = ((sm[0] + sm[1]) + (sm[2] + sm[3])) + ((sm[4] + sm[5]) + (sm[6] + sm[7]));
+                    if (again || !__any_sync(0xffffffffu, !(sum <= kMaxSum))) break;
+                    // a score far above its row's reference: the reference moves (once P V of the first half
+                    // is done, in the second)
+                    if (h == 1) {
+                        ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarH + q), (uint32_t)(i & 1), abort_flag, lim, 50));
+                        if (!ok) break;
+                        tc_fence_after();
                     }
-                };
-                tmem_ld32(ts, xa);
-                tmem_wait32(xa);
-                tmem_ld32(ts + 32, xb);            // in flight while the 32 before are worked on
-                weigh(xa, 0);
-                tmem_wait32(xb);
-                tmem_ld32(ts + 64, xa);
-                weigh(xb, 1);
-                tmem_wait32(xa);
-                tmem_ld32(ts + 96, xb);
-                weigh(xa, 2);
-                tmem_wait32(xb);
-                weigh(xb, 3);
-                float sm[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) attn::f2unpack(acc[e], sm[2 * e], sm[2 * e + 1]);
-                sum = ((sm[0] + sm[1]) + (sm[2] + sm[3])) + ((sm[4] + sm[5]) + (sm[6] + sm[7]));
-                if (look || !__any_sync(0xffffffffu, !(sum <= kMaxSum))) break;
-                look = true;
+                    look_up(2 * h);
+                    again = true;
+                }
+                if (!ok) break;
+                l += sum;
+                attn::tmem_st16u(ts + 64u * h, pk);
+                attn::tmem_st16u(ts + 64u * h + 16u, pk + 16);
+                attn::tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kBarP + 2 * q + h));
             }
-            l += sum;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) attn::tmem_st16u(ts + 16u * c, pk + 16 * c);
-            attn::tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarP + q));
+            if (!ok) break;
             ++i;
         }
         if (ok && i > 0) {
