@@ -74,9 +74,10 @@ bool make_map(CUtensorMap* map, const void* ptr, int d, int H, long long T, int 
 //     2^30, so later tiles need no maximum and O is hardly ever rescaled (the division by the
 //     running sum at the end is right for any m);
 //   P in bf16 over the score columns it came from, O_q += P_q V with P as the A operand.
-// Warp 8 issues the MMAs in the order PV_0(j-1) S_0(j) PV_1(j-1) S_1(j), so that the tensor
-// cores work for one tile while the other's softmax runs; they execute in order, so S_q(j)
-// may overwrite P_q(j-1), and "scores ready" of step j also says that PV_q(j-1) is done.
+// S and P of a query tile have two buffers of 64 keys (P over the scores that it came from), the
+// halves of a 128-key tile.  Warp 8 issues, half by half, PV_0(j-1) S_0(j) PV_1(j-1) S_1(j); the
+// tensor cores execute in order, so S(j) may overwrite P(j-1) of its half, and while a softmax
+// weighs one half, the other half's next scores are on their way.
 // Warp 9 keeps K (3 stages) and V (2 stages) coming by TMA.  Key tiles are counted from the
 // window's first key, sink tiles before them when the two do not touch, so no key is visited
 // twice; a tile that a query tile sees nothing of is skipped for it.  Every wait is bounded.
@@ -96,10 +97,11 @@ constexpr uint32_t kOffK = kOffQ + 2 * kOp;
 constexpr uint32_t kOffV = kOffK + kKStages * kOp;
 constexpr uint32_t kOffBar = kOffV + kVStages * kOp;
 enum : uint32_t { kBarQ = 0, kBarKFull = 1, kBarKFree = kBarKFull + kKStages, kBarVFull = kBarKFree + kKStages,
-                  kBarVFree = kBarVFull + kVStages, kBarS = kBarVFree + kVStages,   // [2] scores ready
-                  kBarP = kBarS + 2,           // [2][2] half of P written, O rescaled (an arrival per softmax warp)
-                  kBarH = kBarP + 4,           // [2] P V of a step's first half done
-                  kBarO = kBarH + 2,           // [2] last P V of the tile done
+                  kBarVFree = kBarVFull + kVStages, // [query tile][half of the key tile]:
+                  kBarS = kBarVFree + kVStages,          // scores ready
+                  kBarP = kBarS + 4,           // P written, O rescaled (one arrival per softmax warp)
+                  kBarH = kBarP + 4,           // P V done
+                  kBarO = kBarH + 4,           // [2] last P V of the tile done
                   kBarDrain = kBarO + 2,       // every MMA done
                   kNumBars = kBarDrain + 1 };
 constexpr uint32_t kOffAbort = kOffBar + 8u * kNumBars;
@@ -107,9 +109,9 @@ constexpr uint32_t kOffTmemSlot = kOffAbort + 8u;
 constexpr uint32_t kSmemBytes = kOffTmemSlot + 16u + 1024u;      // + slack for 1024-byte alignment
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColO = 256;     // + 128 q each
+constexpr uint32_t kColS = 0, kColO = 256;     // + 128 q each; S: two buffers of 64 columns
 constexpr float kMaxSum = 1073741824.0f;       // of a row's weights in a tile, before its reference moves
-constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
+constexpr uint32_t kIdS = idesc_bf16(128, 64, false, false);
 
 struct Args {
     const int* lengths;
@@ -321,37 +323,40 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (!ok) break;
                 const uint64_t vdesc = v0desc + sv * (kOp >> 4), kdesc = k0desc + sk * (kOp >> 4);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    if (dopv[q]) {
-                        // a K step of 16 keys: 8 columns of P (whose halves lie 64 columns apart), 2048 bytes
-                        // (128 descriptor units) of V
+                for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
+                    for (int q = 0; q < 2; ++q) {
+                        const uint32_t s = tmem + kColS + 128u * q + 64u * h;
+                        if (dopv[q]) {
                             ok = ok && mbar_wait(bar(kBarP + 2 * q + h), steps[q] & 1u, abort_flag, lim, 45);
                             if (!ok) break;
                             tc_fence_after();
+                            // a K step of 16 keys: 8 columns of P, 2048 bytes (128 descriptor units) of V
 #pragma unroll
                             for (int ks = 0; ks < kBN / 32; ++ks)
-                                mma_bf16_tmem_a(tmem + kColO + 128u * q, tmem + kColS + 128u * q + 64u * h + 8u * ks,
-                                                vdesc + 128u * (4 * h + ks), idpv, (steps[q] > 0 || h + ks > 0) ? 1u : 0u);
-                            if (h == 0) mma_commit(bar(kBarH + q));
+                                mma_bf16_tmem_a(tmem + kColO + 128u * q, s + 8u * ks, vdesc + 128u * (4 * h + ks), idpv,
+                                                (steps[q] > 0 || h + ks > 0) ? 1u : 0u);
+                            mma_commit(bar(kBarH + 2 * q + h));
+                            if (h == 1) {
+                                ++steps[q];
+                                if (q == 1 || !dopv[1]) mma_commit(bar(kBarVFree + sv));
+                                if (j == p.end[q]) mma_commit(bar(kBarO + q));
+                            }
                         }
-                        if (!ok) break;
-                        ++steps[q];
-                        if (q == 1 || !dopv[1]) mma_commit(bar(kBarVFree + sv));
-                        if (j == p.end[q]) mma_commit(bar(kBarO + q));
-                    }
-                    if (doqk[q]) {
-                        const uint64_t qdesc = q0desc + q * (kOp >> 4);
-                        // a K step of 16 head elements: 32 bytes inside a box, four of them per box
+                        if (doqk[q]) {
+                            // keys 64 h .. of the tile (8192 bytes on); a K step of 16 head elements: 32 bytes inside a
+                            // box, four of them per box
+                            const uint64_t qdesc = q0desc + q * (kOp >> 4), kd = kdesc + 512u * h;
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            if (ks < nks)
-                                mma_bf16(tmem + kColS + 128u * q, qdesc + (ks >> 2) * (kBox >> 4) + 2u * (ks & 3),
-                                         kdesc + (ks >> 2) * (kBox >> 4) + 2u * (ks & 3), kIdS, ks > 0);
-                        mma_commit(bar(kBarS + q));
-                        if (q == 1 || !doqk[1]) mma_commit(bar(kBarKFree + sk));
+                            for (int ks = 0; ks < 8; ++ks)
+                                if (ks < nks)
+                                    mma_bf16(s, qdesc + (ks >> 2) * (kBox >> 4) + 2u * (ks & 3),
+                                             kd + (ks >> 2) * (kBox >> 4) + 2u * (ks & 3), kIdS, ks > 0);
+                            mma_commit(bar(kBarS + 2 * q + h));
+                            if (h == 1 && (q == 1 || !doqk[1])) mma_commit(bar(kBarKFree + sk));
+                        }
                     }
+                    if (!ok) break;
                 }
                 if (j >= 1 && ++sv == kVStages) { sv = 0; pv ^= 1u; }
                 if (++sk == kKStages) { sk = 0; pk ^= 1u; }
@@ -377,8 +382,19 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         float m_ref = -INFINITY, l = 0.0f;
         bool ok = true;
         int i = 0;                                            // key tiles taken
-        for (int j = 0; j < p.n; ++j) {
-            if (!(j < first_end || (j >= near && j < end))) continue;
+        // the first tile from j on that this query tile sees
+        auto seen = [&](int j) { return j < first_end ? j : j < near ? near : j; };
+        auto scores = [&](int h, int step) {                  // of half h of its step-th tile
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarS + 2 * q + h), (uint32_t)step & 1u, abort_flag, lim, 47));
+            tc_fence_after();
+            return ok;
+        };
+        float xa[32], xb[32];
+        // the first look takes both halves, for rows that see nothing of the first one
+        if (end > 0 && scores(0, 0) && scores(1, 0)) tmem_ld32(ts, xa);
+#pragma unroll 1
+        for (int j = seen(0), next; ok && j < end; j = next) {
+            next = seen(j + 1);
             const int s0 = p.start(j);
             const bool sink_tile = j < p.nA;
             // columns [lo, hi] are in the row's window, columns below sk among the sinks
@@ -402,21 +418,17 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     for (int c = 0; c < nbv; ++c) st_shared_v4(v + c * kBox + 16u * r, 0, 0, 0, 0);
                 fence_proxy_async_smem();
             }
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarS + q), (uint32_t)(i & 1), abort_flag, lim, 47));
-            if (!ok) break;
-            tc_fence_after();
-            float xa[32], xb[32];
-            // Moves the references up to the rows' largest scores among columns 32 c0 .. 127 (O is
+            // Moves the references up to the rows' largest scores among columns 32 c0 .. 32 c1 - 1 (O is
             // complete up to here: the P V issued so far are done).
-            auto look_up = [&](int c0) {
+            auto look_up = [&](int c0, int c1) {
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                for (int c = c0; c < 4; ++c) {
-                    tmem_ld32(ts + 32u * c, xa);
-                    tmem_wait32(xa);
-                    mask(xa, c);
+                for (int c = c0; c < c1; ++c) {
+                    tmem_ld32(ts + 32u * c, xb);
+                    tmem_wait32(xb);
+                    mask(xb, c);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) mx[e & 3] = attn::max3f(mx[e & 3], xa[2 * e], xa[2 * e + 1]);
+                    for (int e = 0; e < 16; ++e) mx[e & 3] = attn::max3f(mx[e & 3], xb[2 * e], xb[2 * e + 1]);
                 }
                 const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
                 const float mn = fmaxf(m_ref, mt);
@@ -436,16 +448,29 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                 }
             };
-            if (__any_sync(0xffffffffu, m_ref == -INFINITY)) look_up(0);
             // 2^(x scale - m) without looking for the maximum first: m is a score of an earlier tile, and
-            // float and bf16 hold what is 2^30 times as large as well as what is as large.  Half by half,
-            // so that P V of the first runs beside the second.
+            // float and bf16 hold what is 2^30 times as large as well as what is as large.  The halves
+            // take turns with the tensor cores: while one is weighed, P V of the one before and the next
+            // tile's scores of it run.  At the top the half's first 32 columns are on their way into xa;
+            // the next half's are asked for before the last 32 are weighed.
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 uint32_t pk[32];
                 float sum;
-                bool again = false;
+                bool look = __any_sync(0xffffffffu, m_ref == -INFINITY), looked = false, weighed = false;
                 while (true) {
+                    if (look) {
+                        // (O is rescaled: the P V of the half before has to be done)
+                        if (i + h > 0) {
+                            ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarH + 2 * q + (h ^ 1)),
+                                                                   (uint32_t)(h ? i : i - 1) & 1u, abort_flag, lim, 50));
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+                        look_up(2 * h, i + h == 0 ? 4 : 2 * h + 2);
+                        looked = true;
+                        if (weighed) tmem_ld32(ts + 64u * h, xa);
+                    }
                     const float neg_mr = (m_ref == -INFINITY) ? 0.0f : -m_ref;
                     const uint64_t sc2 = attn::f2pack(a.scale_log2, a.scale_log2), nm2 = attn::f2pack(neg_mr, neg_mr);
                     uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
@@ -466,26 +491,24 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             pk[16 * c + e] = pack_bf16x2(p0, p1);
                         }
                     };
-                    tmem_ld32(ts + 64u * h, xa);
                     tmem_wait32(xa);
-                    tmem_ld32(ts + 64u * h + 32, xb);      // in flight while the 32 before are worked on
+                    tmem_ld32(ts + 64u * h + 32, xb);
                     weigh(xa, 0);
                     tmem_wait32(xb);
+                    // (not across tiles that only the other query tile sees: their MMAs come first, after this P V)
+                    if (h == 0 || (next < end && next == j + 1)) {
+                        if (!scores(h ^ 1, i + h)) break;
+                        tmem_ld32(ts + 64u * (h ^ 1), xa);
+                    }
                     weigh(xb, 1);
                     float sm[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) attn::f2unpack(acc[e], sm[2 * e], sm[2 * e + 1]);
                     sum = ((sm[0] + sm[1]) + (sm[2] + sm[3])) + ((sm[4] + sm[5]) + (sm[6] + sm[7]));
-                    if (again || !__any_sync(0xffffffffu, !(sum <= kMaxSum))) break;
-                    // a score far above its row's reference: the reference moves (once P V of the first half
-                    // is done, in the second)
-                    if (h == 1) {
-                        ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarH + q), (uint32_t)(i & 1), abort_flag, lim, 50));
-                        if (!ok) break;
-                        tc_fence_after();
-                    }
-                    look_up(2 * h);
-                    again = true;
+                    // a sum beyond that: a score far above its row's reference, which moves
+                    look = __any_sync(0xffffffffu, !(sum <= kMaxSum));
+                    weighed = true;
+                    if (looked || !look) break;
                 }
                 if (!ok) break;
                 l += sum;
@@ -498,6 +521,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             if (!ok) break;
             ++i;
+            if (next < end && next > j + 1 && scores(0, i)) tmem_ld32(ts, xa);
         }
         if (ok && i > 0) {
             ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarO + q), 0, abort_flag, lim, 48));

@@ -275,6 +275,9 @@ ATTN = [
     (1, 3, 400, 4, 2, 112, 112, 90, 7, None), (2, 130, 391, 4, 4, 64, 64, 150, 0, [391, 300]),
     (1, 1, 1000, 8, 2, 128, 128, 400, 4, None), (1, 257, 700, 2, 2, 112, 112, 64, 600, None),
     (2, 64, 200, 2, 1, 48, 80, 30, 2, [100, 170]),
+    # query tiles side by side whose windows start in different key tiles, sinks apart from the window
+    (1, 700, 700, 3, 3, 64, 64, 150, 5, None), (2, 900, 900, 1, 1, 112, 112, 1, 130, [900, 640]),
+    (1, 900, 900, 2, 2, 128, 128, 290, 300, None),
 ]
 
 
