@@ -221,6 +221,26 @@ __device__ __forceinline__ Plan make_plan(const Args& a, int n_keys) {
 }
 
 __device__ __forceinline__ uint64_t kmaj(uint32_t addr) { return smem_desc(addr, 16, 1024, kSwizzle128); }
+// The issuing thread's wait: polls without suspending (a suspended thread takes ~300 cycles to resume,
+// which here would stand between a softmax and its next scores), bounded like every wait.
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns,
+                                          int code) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1; !mbar_test_wait(bar, parity); ++it) {
+        if ((it & 255u) == 0) {
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (*abort) return false;
+            if (now - t0 > limit_ns) {
+                *abort = 1;
+                atomicCAS(&g_device_status, 0, code);
+                return false;
+            }
+        }
+    }
+    return true;
+}
+
 // One MMA of the calling thread whose A operand is in TMEM (row m in lane m, a bf16 pair per column).
 __device__ __forceinline__ void mma_bf16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                                 uint32_t accumulate) {
@@ -313,13 +333,13 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const uint64_t v0desc = smem_desc(base + kOffV, kBox, 1024, kSwizzle128);
             uint32_t sk = 0, pk = 0, sv = 0, pv = 0;       // stage and phase of K(j) and of V(j - 1)
             uint32_t steps[2] = {0, 0};                    // key tiles whose P V was issued
-            bool ok = mbar_wait(bar(kBarQ), 0, abort_flag, lim, 43);
+            bool ok = mbar_poll(bar(kBarQ), 0, abort_flag, lim, 43);
 #pragma unroll 1
             for (int j = 0; ok && j <= p.n; ++j) {
                 const bool dopv[2] = {j >= 1 && p.active(0, j - 1), j >= 1 && p.active(1, j - 1)};
                 const bool doqk[2] = {j < p.n && p.active(0, j), j < p.n && p.active(1, j)};
-                if (j >= 1) ok = mbar_wait(bar(kBarVFull + sv), pv, abort_flag, lim, 44);
-                if (j < p.n) ok = ok && mbar_wait(bar(kBarKFull + sk), pk, abort_flag, lim, 46);
+                if (j >= 1) ok = mbar_poll(bar(kBarVFull + sv), pv, abort_flag, lim, 44);
+                if (j < p.n) ok = ok && mbar_poll(bar(kBarKFull + sk), pk, abort_flag, lim, 46);
                 if (!ok) break;
                 const uint64_t vdesc = v0desc + sv * (kOp >> 4), kdesc = k0desc + sk * (kOp >> 4);
 #pragma unroll
@@ -328,7 +348,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     for (int q = 0; q < 2; ++q) {
                         const uint32_t s = tmem + kColS + 128u * q + 64u * h;
                         if (dopv[q]) {
-                            ok = ok && mbar_wait(bar(kBarP + 2 * q + h), steps[q] & 1u, abort_flag, lim, 45);
+                            ok = ok && mbar_poll(bar(kBarP + 2 * q + h), steps[q] & 1u, abort_flag, lim, 45);
                             if (!ok) break;
                             tc_fence_after();
                             // a K step of 16 keys: 8 columns of P, 2048 bytes (128 descriptor units) of V
