@@ -86,9 +86,9 @@ namespace tc {
 using namespace sm100;
 
 constexpr int kBM = 128, kBN = 128;            // queries per tile, keys per tile
-constexpr int kSoftWarps = 8;                  // four per query tile
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kThreads = 320;
+constexpr int kTileWarps = 8;                  // softmax warps per query tile: two threads per row
+constexpr int kMmaWarp = 2 * kTileWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kLoadWarp + 1);
 constexpr uint32_t kBox = 128u * 128u;         // one 64-column SW128 box of 128 rows
 constexpr uint32_t kOp = 2u * kBox;            // a 128 x (d <= 128) operand
 constexpr int kKStages = 3, kVStages = 2;
@@ -102,11 +102,16 @@ enum : uint32_t { kBarQ = 0, kBarKFull = 1, kBarKFree = kBarKFull + kKStages, kB
                   kBarP = kBarS + 4,           // P written, O rescaled (one arrival per softmax warp)
                   kBarH = kBarP + 4,           // P V done
                   kBarO = kBarH + 4,           // [2] last P V of the tile done
-                  kBarDrain = kBarO + 2,       // every MMA done
+                  kBarL = kBarO + 2,           // a half's sums written
+                  kBarDrain = kBarL + 4,       // every MMA done
                   kNumBars = kBarDrain + 1 };
+__host__ __device__ constexpr uint32_t bar_count(uint32_t i) {
+    return ((i >= kBarP && i < kBarP + 4) || (i >= kBarL && i < kBarL + 4)) ? 4u : 1u;
+}
 constexpr uint32_t kOffAbort = kOffBar + 8u * kNumBars;
 constexpr uint32_t kOffTmemSlot = kOffAbort + 8u;
-constexpr uint32_t kSmemBytes = kOffTmemSlot + 16u + 1024u;      // + slack for 1024-byte alignment
+constexpr uint32_t kOffM = kOffTmemSlot + 8u;  // [2][128] the rows' references
+constexpr uint32_t kSmemBytes = kOffM + 2u * kBM * 4u + 1024u;   // + slack for 1024-byte alignment
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;     // + 128 q each; S: two buffers of 64 columns
@@ -274,7 +279,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tmem_relinquish();
     }
     if (tid == 32) {
-        for (uint32_t i = 0; i < kNumBars; ++i) mbar_init(bar(i), (i >= kBarP && i < kBarP + 4) ? 4u : 1u);
+        for (uint32_t i = 0; i < kNumBars; ++i) mbar_init(bar(i), bar_count(i));
         fence_mbar_init();
         *abort_flag = 0;
         tma_prefetch_desc(&tm_q);
@@ -387,41 +392,43 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         __syncwarp();
     } else {
-        // ======================= softmax of tile q, one thread per row =======================
-        const int q = warp >> 2;
+        // ======================= softmax of tile q, two threads per row =======================
+        // Thread 0 of a row has keys 0-63 of each tile, thread 1 keys 64-127.  The row's reference m is both
+        // threads': each weighs with the last it knows, and before it stores its weights (thread 0's of tile
+        // i after thread 1's of tile i - 1, thread 1's after thread 0's of the same tile) it looks whether the
+        // other has moved m meanwhile; whoever moves it rescales O.
+        const int q = warp / kTileWarps, half = (warp >> 2) & 1;
         const int p_lo = q ? p.p_lo[1] : p.p_lo[0], p_hi = q ? p.p_hi[1] : p.p_hi[0];
         const int row0 = q ? p.row0[1] : p.row0[0], head = q ? p.head[1] : p.head[0];
         const int first_end = q ? p.first_end[1] : p.first_end[0], near = q ? p.near[1] : p.near[0];
         const int end = q ? p.end[1] : p.end[0];
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t ts = lane_base + kColS + 128u * q, to = lane_base + kColO + 128u * q;
+        const uint32_t ts = lane_base + kColS + 128u * q, th = ts + 64u * half, to = lane_base + kColO + 128u * q;
+        const uint32_t bar_s = bar(kBarS + 2 * q + half), bar_p = bar(kBarP + 2 * q + half);
+        const uint32_t bar_other = bar(kBarP + 2 * q + (half ^ 1));
         const int row = (warp & 3) * 32 + lane;
         const int t = p_lo + row;                             // this row's position
         const int ws = max(0, t - a.window + 1);
         const bool split = p.startB > 0 || p.nA > 0;
+        volatile float* m_row = reinterpret_cast<volatile float*>(gb + kOffM) + q * kBM + row;
         float m_ref = -INFINITY, l = 0.0f;
-        bool ok = true;
+        bool ok = true, settled = false;                      // settled: every row of the warp has a reference
         int i = 0;                                            // key tiles taken
-        // the first tile from j on that this query tile sees
-        auto seen = [&](int j) { return j < first_end ? j : j < near ? near : j; };
-        auto scores = [&](int h, int step) {                  // of half h of its step-th tile
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarS + 2 * q + h), (uint32_t)step & 1u, abort_flag, lim, 47));
-            tc_fence_after();
+        auto wait = [&](uint32_t b_, uint32_t parity, int code) {
+            ok = __all_sync(0xffffffffu, mbar_wait(b_, parity & 1u, abort_flag, lim, code));
             return ok;
         };
-        float xa[32], xb[32];
-        // the first look takes both halves, for rows that see nothing of the first one
-        if (end > 0 && scores(0, 0) && scores(1, 0)) tmem_ld32(ts, xa);
+        // the first tile from j on that this query tile sees
+        auto seen = [&](int j) { return j < first_end ? j : j < near ? near : j; };
 #pragma unroll 1
-        for (int j = seen(0), next; ok && j < end; j = next) {
-            next = seen(j + 1);
+        for (int j = seen(0); j < end; j = seen(j + 1)) {
             const int s0 = p.start(j);
             const bool sink_tile = j < p.nA;
             // columns [lo, hi] are in the row's window, columns below sk among the sinks
             const int hi = sink_tile ? -1 : min(t, n_keys - 1) - s0;
             const int lo = ws - s0, sk = (split && !sink_tile) ? 0 : min(p.sink, t + 1) - s0;
             const bool masked = __any_sync(0xffffffffu, !((lo <= 0 && hi >= kBN - 1) || sk >= kBN));
-            auto mask = [&](float (&x)[32], int c) {
+            auto mask = [&](float (&x)[32], int c) {          // x: columns 32 c ..
                 if (masked) {
                     const uint32_t keep = (low_bits(hi + 1 - 32 * c) & ~low_bits(lo - 32 * c)) | low_bits(sk - 32 * c);
 #pragma unroll
@@ -429,34 +436,50 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             };
             // rows of padding in V hold anything: zero times that must be zero
-            if (n_keys - s0 < kBN && n_keys < a.Tk) {
+            if (half == 0 && n_keys - s0 < kBN && n_keys < a.Tk) {
                 const uint32_t v = base + kOffV + (uint32_t)(j % kVStages) * kOp;
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarVFull + j % kVStages), (uint32_t)(j / kVStages) & 1u,
-                                                       abort_flag, lim, 49));
-                if (!ok) break;
+                if (!wait(bar(kBarVFull + j % kVStages), (uint32_t)(j / kVStages), 49)) break;
                 for (int r = (n_keys - s0) * 8 + row; r < kBN * 8; r += kBM)
                     for (int c = 0; c < nbv; ++c) st_shared_v4(v + c * kBox + 16u * r, 0, 0, 0, 0);
                 fence_proxy_async_smem();
             }
-            // Moves the references up to the rows' largest scores among columns 32 c0 .. 32 c1 - 1 (O is
-            // complete up to here: the P V issued so far are done).
-            auto look_up = [&](int c0, int c1) {
+            // what the other thread made of the reference, once its weights before these are stored
+            auto follow = [&]() {
+                if (half == 0 && i == 0) return true;
+                if (!wait(bar_other, (uint32_t)(half ? i : i - 1), 51)) return false;
+                const float mn = *m_row;
+                if (mn != m_ref) {
+                    l *= attn::ex2(m_ref - mn);
+                    m_ref = mn;
+                }
+                return true;
+            };
+            // Moves the references up to the rows' largest scores among this thread's columns (the first
+            // look of thread 0 takes both halves, for rows that see nothing of the first).
+            auto look_up = [&]() {
+                const bool first = half == 0 && i == 0;
+                if (first ? !wait(bar(kBarS + 2 * q + 1), 0, 47)
+                          : !wait(bar(kBarH + 2 * q + (half ^ 1)), (uint32_t)(half ? i : i - 1), 50))
+                    return false;                             // (O is complete up to here)
+                tc_fence_after();
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                for (int c = c0; c < c1; ++c) {
-                    tmem_ld32(ts + 32u * c, xb);
-                    tmem_wait32(xb);
-                    mask(xb, c);
+                for (int c = 2 * half; c < (first ? 4 : 2 * half + 2); ++c) {
+                    float x[32];
+                    tmem_ld32(ts + 32u * c, x);
+                    tmem_wait32(x);
+                    mask(x, c);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) mx[e & 3] = attn::max3f(mx[e & 3], xb[2 * e], xb[2 * e + 1]);
+                    for (int e = 0; e < 16; ++e) mx[e & 3] = attn::max3f(mx[e & 3], x[2 * e], x[2 * e + 1]);
                 }
                 const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
                 const float mn = fmaxf(m_ref, mt);
                 const float alpha = mn > m_ref ? attn::ex2(m_ref - mn) : 1.0f;
                 l *= alpha;
                 m_ref = mn;
+                *m_row = mn;
                 // (TMEM accesses are warp-collective: the other rows' alpha is 1)
-                if (i > 0 || c0 > 0) {
+                if (!first) {
 #pragma unroll 1
                     for (int c = 0; c < a.dv / 16; ++c) {
                         float o[16];
@@ -467,90 +490,88 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         attn::tmem_st16(to + 16u * c, o);
                     }
                 }
+                return true;
             };
+            if (!wait(bar_s, (uint32_t)i, 47)) break;
+            tc_fence_after();
+            if (!settled) {
+                if (!follow()) break;
+                if (__any_sync(0xffffffffu, m_ref == -INFINITY) && !look_up()) break;
+                settled = !__any_sync(0xffffffffu, m_ref == -INFINITY);
+            }
             // 2^(x scale - m) without looking for the maximum first: m is a score of an earlier tile, and
-            // float and bf16 hold what is 2^30 times as large as well as what is as large.  The halves
-            // take turns with the tensor cores: while one is weighed, P V of the one before and the next
-            // tile's scores of it run.  At the top the half's first 32 columns are on their way into xa;
-            // the next half's are asked for before the last 32 are weighed.
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                uint32_t pk[32];
-                float sum;
-                bool look = __any_sync(0xffffffffu, m_ref == -INFINITY), looked = false, weighed = false;
-                while (true) {
-                    if (look) {
-                        // (O is rescaled: the P V of the half before has to be done)
-                        if (i + h > 0) {
-                            ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarH + 2 * q + (h ^ 1)),
-                                                                   (uint32_t)(h ? i : i - 1) & 1u, abort_flag, lim, 50));
-                            if (!ok) break;
-                            tc_fence_after();
-                        }
-                        look_up(2 * h, i + h == 0 ? 4 : 2 * h + 2);
-                        looked = true;
-                        if (weighed) tmem_ld32(ts + 64u * h, xa);
-                    }
-                    const float neg_mr = (m_ref == -INFINITY) ? 0.0f : -m_ref;
-                    const uint64_t sc2 = attn::f2pack(a.scale_log2, a.scale_log2), nm2 = attn::f2pack(neg_mr, neg_mr);
-                    uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-                    auto weigh = [&](float (&x)[32], int c) {
-                        mask(x, 2 * h + c);
+            // float and bf16 hold what is 2^30 times as large as well as what is as large.
+            uint32_t pk[32];
+            float sum;
+            bool looked = !settled;
+            while (true) {
+                const float neg_mr = (m_ref == -INFINITY) ? 0.0f : -m_ref;
+                const uint64_t sc2 = attn::f2pack(a.scale_log2, a.scale_log2), nm2 = attn::f2pack(neg_mr, neg_mr);
+                uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const uint64_t y = attn::fma2(attn::f2pack(x[2 * e], x[2 * e + 1]), sc2, nm2);
-                            float p0, p1;
-                            if (e % 8 == 7) {
-                                ex2_fma(y, p0, p1);
-                            } else {
-                                attn::f2unpack(y, p0, p1);
-                                p0 = attn::ex2(p0);
-                                p1 = attn::ex2(p1);
-                            }
-                            acc[e & 3] = attn::add2(acc[e & 3], attn::f2pack(p0, p1));
-                            pk[16 * c + e] = pack_bf16x2(p0, p1);
-                        }
-                    };
-                    tmem_wait32(xa);
-                    tmem_ld32(ts + 64u * h + 32, xb);
-                    weigh(xa, 0);
-                    tmem_wait32(xb);
-                    // (not across tiles that only the other query tile sees: their MMAs come first, after this P V)
-                    if (h == 0 || (next < end && next == j + 1)) {
-                        if (!scores(h ^ 1, i + h)) break;
-                        tmem_ld32(ts + 64u * (h ^ 1), xa);
-                    }
-                    weigh(xb, 1);
-                    float sm[8];
+                for (int c = 0; c < 2; ++c) {
+                    float x[32];
+                    tmem_ld32(th + 32u * c, x);
+                    tmem_wait32(x);
+                    mask(x, 2 * half + c);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) attn::f2unpack(acc[e], sm[2 * e], sm[2 * e + 1]);
-                    sum = ((sm[0] + sm[1]) + (sm[2] + sm[3])) + ((sm[4] + sm[5]) + (sm[6] + sm[7]));
-                    // a sum beyond that: a score far above its row's reference, which moves
-                    look = __any_sync(0xffffffffu, !(sum <= kMaxSum));
-                    weighed = true;
-                    if (looked || !look) break;
+                    for (int e = 0; e < 16; ++e) {
+                        const uint64_t y = attn::fma2(attn::f2pack(x[2 * e], x[2 * e + 1]), sc2, nm2);
+                        float p0, p1;
+                        if (e % 8 == 7) {
+                            ex2_fma(y, p0, p1);
+                        } else {
+                            attn::f2unpack(y, p0, p1);
+                            p0 = attn::ex2(p0);
+                            p1 = attn::ex2(p1);
+                        }
+                        acc[e & 3] = attn::add2(acc[e & 3], attn::f2pack(p0, p1));
+                        pk[16 * c + e] = pack_bf16x2(p0, p1);
+                    }
                 }
-                if (!ok) break;
-                l += sum;
-                attn::tmem_st16u(ts + 64u * h, pk);
-                attn::tmem_st16u(ts + 64u * h + 16u, pk + 16);
-                attn::tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(kBarP + 2 * q + h));
+                float sm[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) attn::f2unpack(acc[e], sm[2 * e], sm[2 * e + 1]);
+                sum = ((sm[0] + sm[1]) + (sm[2] + sm[3])) + ((sm[4] + sm[5]) + (sm[6] + sm[7]));
+                // a reference that the other thread has moved, or a score far above it
+                const float m_old = m_ref;
+                if (half == 1 || i > 0) {
+                    if (!wait(bar_other, (uint32_t)(half ? i : i - 1), 51)) break;
+                    m_ref = *m_row;
+                }
+                const bool stale = m_ref != m_old, far = !(sum <= kMaxSum) && !looked;
+                if (!__any_sync(0xffffffffu, stale || far)) break;
+                l *= stale ? attn::ex2(m_old - m_ref) : 1.0f;
+                if (!__any_sync(0xffffffffu, stale)) {
+                    if (!look_up()) break;
+                    looked = true;
+                }
             }
             if (!ok) break;
+            l += sum;
+            attn::tmem_st16u(th, pk);
+            attn::tmem_st16u(th + 16u, pk + 16);
+            attn::tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_p);
             ++i;
-            if (next < end && next > j + 1 && scores(0, i)) tmem_ld32(ts, xa);
         }
-        if (ok && i > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarO + q), 0, abort_flag, lim, 48));
-            if (ok) {
-                tc_fence_after();
-                const float inv = 1.0f / l;
+        // (thread 0 may have to follow thread 1 once more)
+        if (ok && i > 0 && wait(bar(kBarO + q), 0, 48) && (half == 1 || wait(bar_other, (uint32_t)(i - 1), 51))) {
+            tc_fence_after();
+            if (*m_row != m_ref) l *= attn::ex2(m_ref - *m_row);
+            // the halves' sums meet in Q's place (the tile's last S is done)
+            volatile float* sums = reinterpret_cast<volatile float*>(gb + kOffQ + q * kOp);
+            sums[half * kBM + row] = l;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarL + 2 * q + half));
+            if (wait(bar(kBarL + 2 * q + (half ^ 1)), 0, 54)) {
+                const float inv = 1.0f / (sums[row] + sums[kBM + row]);
+                const int c_mid = a.dv / 32, c_lo = half ? c_mid : 0, c_hi = half ? a.dv / 16 : c_mid;
                 __nv_bfloat16* orow = a.out + (((long long)b * a.Tq + row0 + row) * a.Hq + head) * a.dv;
 #pragma unroll 1
-                for (int c = 0; c < a.dv / 16; ++c) {
+                for (int c = c_lo; c < c_hi; ++c) {
                     float o[16];
                     tmem_ld16(to + 16u * c, o);
                     tmem_wait_ld();
