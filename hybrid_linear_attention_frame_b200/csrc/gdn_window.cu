@@ -154,28 +154,6 @@ __device__ __forceinline__ void tmem_wait32(float (&x)[32]) {
                  :: "memory");
 }
 
-constexpr float kE0 = 9.99928073e-01f, kE1 = 6.93260985e-01f, kE2 = 2.42611125e-01f, kE3 = 5.51716703e-02f;
-
-// 2^y of a pair on the FMA pipe: y = r + f with r whole (adding 1.5 2^23 rounds to it), f in
-// [-1/2, 1/2], 2^f by the cubic that is least off in relative error there (1e-4, a twentieth of the
-// weight's rounding to bf16), r added to the exponent.  y is held in [-126, 127]: far below, the
-// weight is as good as 0; far above, the sum shows it.
-__device__ __forceinline__ void ex2_fma(uint64_t y, float& p0, float& p1) {
-    float y0, y1, r0, r1;
-    attn::f2unpack(y, y0, y1);
-    const uint64_t c = attn::f2pack(fminf(fmaxf(y0, -126.0f), 127.0f), fminf(fmaxf(y1, -126.0f), 127.0f));
-    const uint64_t magic = attn::f2pack(12582912.0f, 12582912.0f), back = attn::f2pack(-12582912.0f, -12582912.0f);
-    const uint64_t r = attn::add2(c, magic);
-    const uint64_t f = attn::fma2(attn::add2(r, back), attn::f2pack(-1.0f, -1.0f), c);
-    uint64_t v = attn::fma2(f, attn::f2pack(kE3, kE3), attn::f2pack(kE2, kE2));
-    v = attn::fma2(v, f, attn::f2pack(kE1, kE1));
-    v = attn::fma2(v, f, attn::f2pack(kE0, kE0));
-    attn::f2unpack(r, r0, r1);
-    attn::f2unpack(v, p0, p1);
-    p0 = __int_as_float(__float_as_int(p0) + (__float_as_int(r0) << 23));
-    p1 = __int_as_float(__float_as_int(p1) + (__float_as_int(r1) << 23));
-}
-
 // the n lowest bits, none below 0, all above 31
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 
@@ -516,15 +494,10 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     mask(x, 2 * half + c);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const uint64_t y = attn::fma2(attn::f2pack(x[2 * e], x[2 * e + 1]), sc2, nm2);
                         float p0, p1;
-                        if (e % 8 == 7) {
-                            ex2_fma(y, p0, p1);
-                        } else {
-                            attn::f2unpack(y, p0, p1);
-                            p0 = attn::ex2(p0);
-                            p1 = attn::ex2(p1);
-                        }
+                        attn::f2unpack(attn::fma2(attn::f2pack(x[2 * e], x[2 * e + 1]), sc2, nm2), p0, p1);
+                        p0 = attn::ex2(p0);
+                        p1 = attn::ex2(p1);
                         acc[e & 3] = attn::add2(acc[e & 3], attn::f2pack(p0, p1));
                         pk[16 * c + e] = pack_bf16x2(p0, p1);
                     }
