@@ -102,7 +102,7 @@ enum : uint32_t { kBarQ = 0, kBarKFull = 1, kBarKFree = kBarKFull + kKStages, kB
                   kBarP = kBarS + 4,           // P written, O rescaled (one arrival per softmax warp)
                   kBarH = kBarP + 4,           // P V done
                   kBarO = kBarH + 4,           // [2] last P V of the tile done
-                  kBarL = kBarO + 2,           // a half's sums written
+                  kBarL = kBarO + 2,           // a row's word written (its maximum, at the end its sum)
                   kBarDrain = kBarL + 4,       // every MMA done
                   kNumBars = kBarDrain + 1 };
 __host__ __device__ constexpr uint32_t bar_count(uint32_t i) {
@@ -110,7 +110,7 @@ __host__ __device__ constexpr uint32_t bar_count(uint32_t i) {
 }
 constexpr uint32_t kOffAbort = kOffBar + 8u * kNumBars;
 constexpr uint32_t kOffTmemSlot = kOffAbort + 8u;
-constexpr uint32_t kOffM = kOffTmemSlot + 8u;  // [2][128] the rows' references
+constexpr uint32_t kOffM = kOffTmemSlot + 8u;  // [2][128] the rows' references, at the end their sums
 constexpr uint32_t kSmemBytes = kOffM + 2u * kBM * 4u + 1024u;   // + slack for 1024-byte alignment
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr uint32_t kTmemCols = 512;
@@ -236,7 +236,7 @@ __device__ __forceinline__ void mma_bf16_tmem_a(uint32_t d_tmem, uint32_t a_tmem
 
 __global__ void __launch_bounds__(kThreads, 1)
 window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v, const Args a)
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const Args a)
 {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -263,6 +263,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
+        tma_prefetch_desc(&tm_o);
     }
     tc_fence_before();
     __syncthreads();
@@ -396,6 +397,21 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             ok = __all_sync(0xffffffffu, mbar_wait(b_, parity & 1u, abort_flag, lim, code));
             return ok;
         };
+        // Both threads of a row end up with join(thread 0's word), computed by thread 1.
+        auto swap = [&](auto&& join, float& word, uint32_t parity) {
+            if (half == 1) {
+                if (!wait(bar(kBarL + 2 * q), parity, 54)) return false;
+                word = join(*m_row);
+            }
+            *m_row = word;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarL + 2 * q + half));
+            if (half == 0) {
+                if (!wait(bar(kBarL + 2 * q + 1), parity, 54)) return false;
+                word = *m_row;
+            }
+            return true;
+        };
         // the first tile from j on that this query tile sees
         auto seen = [&](int j) { return j < first_end ? j : j < near ? near : j; };
 #pragma unroll 1
@@ -432,32 +448,32 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
                 return true;
             };
-            // Moves the references up to the rows' largest scores among this thread's columns (the first
-            // look of thread 0 takes both halves, for rows that see nothing of the first).
-            auto look_up = [&]() {
-                const bool first = half == 0 && i == 0;
-                if (first ? !wait(bar(kBarS + 2 * q + 1), 0, 47)
-                          : !wait(bar(kBarH + 2 * q + (half ^ 1)), (uint32_t)(half ? i : i - 1), 50))
-                    return false;                             // (O is complete up to here)
-                tc_fence_after();
+            // the row's largest score among this thread's columns
+            auto largest = [&]() {
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-                for (int c = 2 * half; c < (first ? 4 : 2 * half + 2); ++c) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
                     float x[32];
-                    tmem_ld32(ts + 32u * c, x);
+                    tmem_ld32(th + 32u * c, x);
                     tmem_wait32(x);
-                    mask(x, c);
+                    mask(x, 2 * half + c);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) mx[e & 3] = attn::max3f(mx[e & 3], x[2 * e], x[2 * e + 1]);
                 }
-                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-                const float mn = fmaxf(m_ref, mt);
+                return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+            };
+            // Moves the references up to it, and O along, once it is complete up to here.
+            auto look_up = [&]() {
+                const bool none = half == 0 && i == 0;        // no P V yet
+                if (!none && !wait(bar(kBarH + 2 * q + (half ^ 1)), (uint32_t)(half ? i : i - 1), 50)) return false;
+                tc_fence_after();
+                const float mn = fmaxf(m_ref, largest());
                 const float alpha = mn > m_ref ? attn::ex2(m_ref - mn) : 1.0f;
                 l *= alpha;
                 m_ref = mn;
                 *m_row = mn;
                 // (TMEM accesses are warp-collective: the other rows' alpha is 1)
-                if (!first) {
+                if (!none) {
 #pragma unroll 1
                     for (int c = 0; c < a.dv / 16; ++c) {
                         float o[16];
@@ -472,7 +488,11 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             };
             if (!wait(bar_s, (uint32_t)i, 47)) break;
             tc_fence_after();
-            if (!settled) {
+            if (i == 0) {
+                m_ref = largest();
+                if (!swap([&](float other) { m_ref = fmaxf(m_ref, other); return m_ref; }, m_ref, 0)) break;
+                settled = !__any_sync(0xffffffffu, m_ref == -INFINITY);
+            } else if (!settled) {
                 if (!follow()) break;
                 if (__any_sync(0xffffffffu, m_ref == -INFINITY) && !look_up()) break;
                 settled = !__any_sync(0xffffffffu, m_ref == -INFINITY);
@@ -533,28 +553,44 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // (thread 0 may have to follow thread 1 once more)
         if (ok && i > 0 && wait(bar(kBarO + q), 0, 48) && (half == 1 || wait(bar_other, (uint32_t)(i - 1), 51))) {
             tc_fence_after();
-            if (*m_row != m_ref) l *= attn::ex2(m_ref - *m_row);
-            // the halves' sums meet in Q's place (the tile's last S is done)
-            volatile float* sums = reinterpret_cast<volatile float*>(gb + kOffQ + q * kOp);
-            sums[half * kBM + row] = l;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarL + 2 * q + half));
-            if (wait(bar(kBarL + 2 * q + (half ^ 1)), 0, 54)) {
-                const float inv = 1.0f / (sums[row] + sums[kBM + row]);
-                const int c_mid = a.dv / 32, c_lo = half ? c_mid : 0, c_hi = half ? a.dv / 16 : c_mid;
-                __nv_bfloat16* orow = a.out + (((long long)b * a.Tq + row0 + row) * a.Hq + head) * a.dv;
-#pragma unroll 1
-                for (int c = c_lo; c < c_hi; ++c) {
+            if (half == 0 && *m_row != m_ref) l *= attn::ex2(m_ref - *m_row);
+            float total = l;
+            if (swap([&](float other) { return l + other; }, total, 1)) {
+                // thread `half` of a row takes 64 columns, one box; O / l in bf16 goes out through the tile's
+                // place in Q (its last S is done), 32 rows a warp by one copy, which leaves rows past the
+                // last query alone.  A tile that `lengths` cuts short writes its rows one by one.
+                const float inv = 1.0f / total;
+                const int groups = min(4, a.dv / 16 - 4 * half);
+                const bool cut = p_hi + 1 < a.Tk - a.Tq + min(row0 + kBM, a.Tq);
+                const uint32_t stage = base + kOffQ + q * kOp + half * kBox + (uint32_t)row * 128u;
+                __nv_bfloat16* orow = a.out + (((long long)b * a.Tq + row0 + row) * a.Hq + head) * a.dv + 64 * half;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c >= groups) break;
                     float o[16];
-                    tmem_ld16(to + 16u * c, o);
+                    tmem_ld16(to + 64u * half + 16u * c, o);
                     tmem_wait_ld();
-                    if (t <= p_hi) {
-                        uint4* dst = reinterpret_cast<uint4*>(orow + 16 * c);
-                        dst[0] = make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
-                                            pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
-                        dst[1] = make_uint4(pack_bf16x2(o[8] * inv, o[9] * inv), pack_bf16x2(o[10] * inv, o[11] * inv),
-                                            pack_bf16x2(o[12] * inv, o[13] * inv), pack_bf16x2(o[14] * inv, o[15] * inv));
+                    uint32_t w[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+                    if (!cut) {
+                        st_shared_v4(stage + (uint32_t)(((2 * c) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+                        st_shared_v4(stage + (uint32_t)(((2 * c + 1) ^ (row & 7)) << 4), w[4], w[5], w[6], w[7]);
+                    } else if (t <= p_hi) {
+                        reinterpret_cast<uint4*>(orow + 16 * c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        reinterpret_cast<uint4*>(orow + 16 * c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
                     }
+                }
+                const int first = row0 + 32 * (warp & 3);
+                if (!cut && groups > 0 && first < a.Tq) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_4d(&tm_o, stage, 64 * half, head, first, b);
+                        bulk_commit_group();
+                        bulk_wait_group_read0();
+                    }
+                    __syncwarp();
                 }
             }
         }
@@ -951,8 +987,10 @@ window_append_kernel(const AppendArgs a)
 cudaError_t launch_window(const WindowArgs& a, cudaStream_t stream)
 {
     using namespace window::tc;
-    CUtensorMap mq, mk, mv;
-    if (!window::make_map(&mq, a.q, a.dk, a.Hq, a.Tq, a.B, kBM, a.q_head, a.q_row, a.q_batch) ||
+    CUtensorMap mq, mk, mv, mo;
+    const long long orow = (long long)a.Hq * a.dv;
+    if (!window::make_map(&mo, a.out, a.dv, a.Hq, a.Tq, a.B, 32, a.dv, orow, orow * a.Tq) ||
+        !window::make_map(&mq, a.q, a.dk, a.Hq, a.Tq, a.B, kBM, a.q_head, a.q_row, a.q_batch) ||
         !window::make_map(&mk, a.k, a.dk, a.Hkv, a.Tk, a.B, kBM, a.k_head, a.k_row, a.k_batch) ||
         !window::make_map(&mv, a.v, a.dv, a.Hkv, a.Tk, a.B, kBM, a.v_head, a.v_row, a.v_batch))
         return cudaErrorInvalidValue;
@@ -972,7 +1010,7 @@ cudaError_t launch_window(const WindowArgs& a, cudaStream_t stream)
     r.wait_limit_ns = g_wait_limit_ns;
     const long long blocks = (long long)r.row_blocks * r.head_blocks;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    window_attn_kernel<<<dim3((unsigned)blocks, (unsigned)a.B), kThreads, kSmemBytes, stream>>>(mq, mk, mv, r);
+    window_attn_kernel<<<dim3((unsigned)blocks, (unsigned)a.B), kThreads, kSmemBytes, stream>>>(mq, mk, mv, mo, r);
     return cudaGetLastError();
 }
 
