@@ -51,6 +51,12 @@ __device__ __forceinline__ float softplus_series(float x) {
     return fmaf(2.0f * s, r, fmaxf(x, 0.0f));
 }
 
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 // v silu(g); the quotient of a gate far below 0 is 0
 __device__ __forceinline__ float gated(float v, float g) { return v * __fdividef(g, 1.0f + attn::ex2(-g * kLog2e)); }
 
@@ -92,7 +98,7 @@ constexpr int kTile = 64;                  // tokens per tile
 constexpr int kScanThreads = kC * kL;      // 128: warps 0-3; the helpers are warps 4-7
 constexpr int kThreads = 2 * kScanThreads;
 static_assert(kScanThreads == kTile * 2, "a helper thread has one token and 8 channels of a tile");
-constexpr int kDRow = kTile + 2;           // (delta, delta x) pairs per channel, padded off the banks
+constexpr int kDRow = kTile + 2;           // (delta, delta x) per channel, padded off the banks
 constexpr int kYRow = 20;                  // sums per token: 16 channels, padded so that 8 tokens x 4
                                            // channels, a warp's store, fall on 32 banks
 enum { kFull = 1, kEmpty = 3, kYFull = 5, kYEmpty = 7 };   // named barriers, + buffer
@@ -108,16 +114,102 @@ __device__ __forceinline__ void bar_sync(int id) {
     asm volatile("bar.sync %0, %1;" :: "r"(id), "n"(kThreads) : "memory");
 }
 
-// S floats per thread from / to shared or global memory
-template <int S> __device__ __forceinline__ void ld(float (&r)[S], const float* p) {
-    if constexpr (S == 1) r[0] = *p;
-    else if constexpr (S == 2) { const float2 v = *reinterpret_cast<const float2*>(p); r[0] = v.x; r[1] = v.y; }
-    else {
+// B and C of a tile: a row of 2 N floats per token, in units of 16 bytes.  Thread l of a channel reads
+//   S = 1: half a unit (B, C);   S = 2: a unit (B, B, C, C);
+//   S = 4, 8: units of B, then of C, the j-th of every thread side by side,
+// so that the 8 threads' units are one contiguous line; and the rows are swizzled so that the helpers'
+// stores, a few rows at a time, fall on all banks too.
+template <int S> __device__ __forceinline__ constexpr int unit_at(int t, int unit) {
+    return S == 1 ? unit ^ ((t >> 1) & 3) : S == 2 ? unit ^ (t & 3) : S == 4 ? unit ^ (t & 1) : unit;
+}
+
+// What a thread needs of two tokens: (delta, delta x) of each, S values of B and S of C as pairs of f32
+// in 64-bit registers.  The loads are written out so that they stay where they are put, some tokens
+// ahead of their use.
+template <int S> struct Tokens {
+    static constexpr int P = S > 1 ? S / 2 : 1;
+    float de[2], dx[2];
+    uint64_t B[2][P], C[2][P];
+    // d: this channel's pairs from the first token on, bc: its row; t: the token within its 8
+    __device__ void load(uint32_t d, uint32_t bc, int t, int l) {
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(de[0]), "=f"(dx[0]), "=f"(de[1]), "=f"(dx[1]) : "r"(d));
 #pragma unroll
-        for (int i = 0; i < S; i += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(p + i);
-            r[i] = v.x; r[i + 1] = v.y; r[i + 2] = v.z; r[i + 3] = v.w;
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t row = bc + 8 * (S * kL) * k;
+            if constexpr (S == 1) {
+                asm volatile("ld.shared.b64 %0, [%1];"
+                             : "=l"(B[k][0]) : "r"(row + 16 * unit_at<1>(t + k, l >> 1) + 8 * (l & 1)));
+            } else if constexpr (S == 2) {
+                lds(row + 16 * unit_at<2>(t + k, l), B[k][0], C[k][0]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < S / 4; ++j) {
+                    lds(row + 16 * (8 * j + unit_at<S>(t + k, l)), B[k][2 * j], B[k][2 * j + 1]);
+                    lds(row + 16 * (8 * (S / 4 + j) + unit_at<S>(t + k, l)), C[k][2 * j], C[k][2 * j + 1]);
+                }
+            }
         }
+    }
+    __device__ static void lds(uint32_t a, uint64_t& x, uint64_t& y) {
+        asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(a));
+    }
+};
+
+// S states of one channel, in pairs for the paired FMA.
+template <int S> struct States {
+    static constexpr int P = S > 1 ? S / 2 : 1;
+    uint64_t h[P], A[P];
+    __device__ void init(const float* a, const float* h0) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int j = S > 1 ? 2 * i + 1 : 0;
+            A[i] = a ? attn::f2pack(a[2 * i] * kLog2e, a[j] * kLog2e) : 0ull;
+            h[i] = h0 ? attn::f2pack(h0[2 * i], h0[j]) : 0ull;
+        }
+    }
+    // one token; returns this thread's part of C . h
+    __device__ float step(const Tokens<S>& t, int k) {
+        float s0, s1;
+        if constexpr (S == 1) {
+            float B, C, a1, hv, _;
+            attn::f2unpack(t.B[k][0], B, C);
+            attn::f2unpack(A[0], a1, _);
+            attn::f2unpack(h[0], hv, _);
+            hv = fmaf(attn::ex2(t.de[k] * a1), hv, t.dx[k] * B);
+            h[0] = attn::f2pack(hv, hv);
+            return hv * C;
+        }
+        const uint64_t de = attn::f2pack(t.de[k], t.de[k]), dx = attn::f2pack(t.dx[k], t.dx[k]);
+        uint64_t s = 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            attn::f2unpack(mul2(de, A[i]), s0, s1);
+            h[i] = attn::fma2(attn::f2pack(attn::ex2(s0), attn::ex2(s1)), h[i], mul2(dx, t.B[k][i]));
+            s = i == 0 ? mul2(h[i], t.C[k][i]) : attn::fma2(h[i], t.C[k][i], s);
+        }
+        attn::f2unpack(s, s0, s1);
+        return s0 + s1;
+    }
+    __device__ void store(float* o) const {
+        float a, b;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            attn::f2unpack(h[i], a, b);
+            o[2 * i] = a;
+            if (S > 1) o[2 * i + 1] = b;
+        }
+    }
+};
+
+// One round of the sum over a channel's 8 threads: of 2 w tokens' parts each thread keeps w, those of
+// its own bit w, with its partner's added; after rounds 4, 2, 1 thread l has token l's sum.
+template <int W> __device__ __forceinline__ void sum_round(float (&v)[8], int l) {
+    const bool up = (l & W) != 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        const float keep = up ? v[i + W] : v[i], give = up ? v[i] : v[i + W];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, W);
     }
 }
 
@@ -126,6 +218,7 @@ __global__ void __launch_bounds__(kThreads)
 selective_scan_kernel(const ScanArgs a)
 {
     constexpr int S = N / kL;
+    constexpr int kRing = S == 8 ? 2 : 4;                                // pairs of tokens
     extern __shared__ __align__(16) uint8_t smem[];
     float2* s_d = reinterpret_cast<float2*>(smem);                       // [2][kC][kDRow]
     float* s_bc = reinterpret_cast<float*>(s_d + 2 * kC * kDRow);        // [2][kTile][kL][B: S | C: S]
@@ -138,61 +231,48 @@ selective_scan_kernel(const ScanArgs a)
         // ======================= the states =======================
         const int tid = threadIdx.x, l = tid % kL, ch = tid / kL, c = c0 + ch;
         const bool live = c < a.D;
-        float h[S], A[S];
+        States<S> s;
         const long long so = ((long long)b * a.D + c) * N + l * S;
-#pragma unroll
-        for (int i = 0; i < S; ++i) {
-            h[i] = (live && a.state_in) ? a.state_in[so + i] : 0.0f;
-            A[i] = live ? a.A[(long long)c * N + l * S + i] * kLog2e : 0.0f;
-        }
+        s.init(live ? a.A + (long long)c * N + l * S : nullptr, (live && a.state_in) ? a.state_in + so : nullptr);
         for (int k = 0; k < tiles; ++k) {
             const int buf = k & 1;
-            const float2* d = s_d + (buf * kC + ch) * kDRow;
-            const float* bc = s_bc + buf * kTile * 2 * N + l * 2 * S;
-            float* y = s_y + buf * kTile * kYRow + ch;
+            const uint32_t d = sm100::smem_u32(s_d + (buf * kC + ch) * kDRow);
+            const uint32_t bc = sm100::smem_u32(s_bc + buf * kTile * 2 * N);
+            float* y = s_y + buf * kTile * kYRow + ch + l * kYRow;
             bar_sync(kFull + buf);
             if (k >= 2) bar_sync(kYEmpty + buf);
+            // A ring of tokens, loaded kRing - 1 ahead (past the tile's end: other data of this block's
+            // shared memory, not used); the sum of one group of 8 goes on beside the next group's tokens.
+            Tokens<S> ring[kRing];
+#pragma unroll
+            for (int u = 0; u < kRing - 1; ++u) ring[u].load(d + 16 * u, bc + 16 * N * u, 2 * u, l);
             const int groups = (min(kTile, n - k * kTile) + 7) / 8;
+            float last[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll 1
             for (int g = 0; g < groups; ++g) {
                 float v[8];
 #pragma unroll
-                for (int t = 0; t < 8; t += 2) {
-                    const float4 dd = *reinterpret_cast<const float4*>(d + g * 8 + t);
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const float de = u ? dd.z : dd.x, dx = u ? dd.w : dd.y;
-                        float B[S], C[S];
-                        ld<S>(B, bc + (g * 8 + t + u) * 2 * N);
-                        ld<S>(C, bc + (g * 8 + t + u) * 2 * N + S);
-                        float s = 0.0f;
-#pragma unroll
-                        for (int i = 0; i < S; ++i) {
-                            h[i] = fmaf(attn::ex2(de * A[i]), h[i], dx * B[i]);
-                            s = i == 0 ? h[i] * C[i] : fmaf(h[i], C[i], s);
-                        }
-                        v[t + u] = s;
-                    }
+                for (int u = 0; u < 4; ++u) {
+                    const int ahead = u + kRing - 1;
+                    ring[ahead % kRing].load(d + 16 * (4 * g + ahead), bc + 16 * N * (4 * g + ahead), 2 * ahead & 7, l);
+                    v[2 * u] = s.step(ring[u % kRing], 0);
+                    v[2 * u + 1] = s.step(ring[u % kRing], 1);
+                    if (u == 0) sum_round<4>(last, l);
+                    if (u == 1) sum_round<2>(last, l);
+                    if (u == 2) sum_round<1>(last, l);
+                    if (u == 3 && g > 0) y[8 * (g - 1) * kYRow] = last[0];
                 }
-                // the 8 threads of a channel sum 8 tokens, one left with each: thread l ends with token l
 #pragma unroll
-                for (int w = 4; w > 0; w >>= 1) {
-                    const bool up = (l & w) != 0;
-#pragma unroll
-                    for (int i = 0; i < w; ++i) {
-                        const float keep = up ? v[i + w] : v[i], give = up ? v[i] : v[i + w];
-                        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, w);
-                    }
-                }
-                y[(g * 8 + l) * kYRow] = v[0];
+                for (int t = 0; t < 8; ++t) last[t] = v[t];
             }
+            sum_round<4>(last, l);
+            sum_round<2>(last, l);
+            sum_round<1>(last, l);
+            y[8 * (groups - 1) * kYRow] = last[0];
             bar_arrive(kYFull + buf);
             if (k + 2 < tiles) bar_arrive(kEmpty + buf);
         }
-        if (live && a.state_out) {
-#pragma unroll
-            for (int i = 0; i < S; ++i) a.state_out[so + i] = h[i];
-        }
+        if (live && a.state_out) s.store(a.state_out + so);
     } else {
         // ======================= rows in, rows out =======================
         const int tid = threadIdx.x - kScanThreads, row = tid >> 1, cv = 8 * (tid & 1), c = c0 + cv;
@@ -234,7 +314,10 @@ selective_scan_kernel(const ScanArgs a)
             const int buf = k & 1, t = k * kTile + row;
             bar_sync(kYFull + buf);
             float f[8];
-            ld<8>(f, s_y + (buf * kTile + row) * kYRow + cv);
+            const float4* v = reinterpret_cast<const float4*>(s_y + (buf * kTile + row) * kYRow + cv);
+            const float4 v0 = v[0], v1 = v[1];
+            f[0] = v0.x; f[1] = v0.y; f[2] = v0.z; f[3] = v0.w;
+            f[4] = v1.x; f[5] = v1.y; f[6] = v1.z; f[7] = v1.w;
             if (k + 2 < tiles) bar_arrive(kYEmpty + buf);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -261,11 +344,23 @@ selective_scan_kernel(const ScanArgs a)
             for (int i = 0; i < kBC; ++i) {
                 const int p = tid + i * kScanThreads;
                 if (p < kTile * N / 8) {
-                    float* w = s_bc + (buf * kTile + p / (N / 8)) * 2 * N + (p % (N / 8)) * 16;
+                    const int pt = p / (N / 8), pu = p % (N / 8);
+                    float4* w = reinterpret_cast<float4*>(s_bc + (buf * kTile + pt) * 2 * N);
+                    const auto& B = rb[i];
+                    const auto& C = rc[i];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        w[(e / S) * 2 * S + e % S] = rb[i].get(e);
-                        w[(e / S) * 2 * S + S + e % S] = rc[i].get(e);
+                    for (int u = 0; u < 4; ++u) {
+                        if constexpr (S == 1)
+                            w[unit_at<1>(pt, u)] = make_float4(B.get(2 * u), C.get(2 * u), B.get(2 * u + 1), C.get(2 * u + 1));
+                        else if constexpr (S == 2)
+                            w[unit_at<2>(pt, 4 * pu + u)] =
+                                make_float4(B.get(2 * u), B.get(2 * u + 1), C.get(2 * u), C.get(2 * u + 1));
+                        else {
+                            // states 4 (u & 1) .. of the 8: unit j of thread l
+                            const auto& V = u < 2 ? B : C;
+                            const int s4 = 2 * pu + (u & 1), l = s4 * 4 / S, j = s4 % (S / 4) + (u < 2 ? 0 : S / 4), e = 4 * (u & 1);
+                            w[8 * j + unit_at<S>(pt, l)] = make_float4(V.get(e), V.get(e + 1), V.get(e + 2), V.get(e + 3));
+                        }
                     }
                 }
             }
