@@ -5,11 +5,12 @@
 // rows before the call's first token taken from state_in (its last W - 1 inputs, oldest
 // first; zeros without one).  state_out receives the last W - 1 inputs of each sequence.
 //
-// 2 W + 5 operations per element against 2 elements of traffic: bound by HBM.  A thread
-// owns one 16-byte vector of channels and walks kStretch tokens with the last W - 1 rows in
-// registers, so x is read once but for the W - 1 rows of halo per stretch; the loads of
-// kBatch rows are issued before the first is used.  Channels are the fastest thread index,
-// so a warp reads and writes 512 contiguous bytes of a row.
+// 2 W + 5 operations and two special functions (the SiLU) per element against two elements of
+// traffic: bound by HBM, with the special-function unit busy for 0.7 of that time, so loads and
+// arithmetic have to overlap.  A thread owns 4 channels, few enough that 7 to 9 blocks of 128 threads
+// share an SM, and walks kStretch tokens with the last W - 1 rows in registers; x is read once but for
+// the W - 1 rows of halo per stretch, and the loads of kBatch rows are issued before the first is
+// used.  Channels are the fastest thread index, so a warp reads and writes whole lines of a row.
 #include "gdn_common.cuh"
 #include "gdn_sm100.cuh"
 
@@ -30,30 +31,33 @@ struct ConvArgs {
 namespace conv {
 
 constexpr int kThreads = 128;
-constexpr int kStretch = 16;   // tokens per thread; a stretch is longer than the halo, so that only
+constexpr int kStretch = 32;   // tokens per thread; a stretch is longer than the halo, so that only
                                // stretch 0 reads state_in and state_out may be the same memory
 constexpr int kBatch = 8;
+constexpr int V = 4;           // channels per thread
 
-// A 16-byte vector of channels as pairs of f32 in 64-bit registers, the form of the paired FMA.
+// Four channels as they lie in memory, and as two pairs of f32 in 64-bit registers, the form of the
+// paired FMA.
 template <typename IOT> struct Vec;
 template <> struct Vec<__nv_bfloat16> {
-    static constexpr int n = 8;
-    __device__ static uint64_t pair(const uint4& v, int i) {
-        const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    using Raw = uint2;
+    __device__ static Raw zero() { return make_uint2(0, 0); }
+    __device__ static uint64_t pair(const Raw& v, int i) {
+        const uint32_t w = i == 0 ? v.x : v.y;
         return attn::f2pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     }
-    __device__ static uint4 pack(const float (&f)[8]) {
-        return make_uint4(sm100::pack_bf16x2(f[0], f[1]), sm100::pack_bf16x2(f[2], f[3]),
-                          sm100::pack_bf16x2(f[4], f[5]), sm100::pack_bf16x2(f[6], f[7]));
+    __device__ static Raw pack(const float (&f)[V]) {
+        return make_uint2(sm100::pack_bf16x2(f[0], f[1]), sm100::pack_bf16x2(f[2], f[3]));
     }
 };
 template <> struct Vec<float> {
-    static constexpr int n = 4;
-    __device__ static uint64_t pair(const uint4& v, int i) {
+    using Raw = uint4;
+    __device__ static Raw zero() { return make_uint4(0, 0, 0, 0); }
+    __device__ static uint64_t pair(const Raw& v, int i) {
         return i == 0 ? attn::f2pack(__uint_as_float(v.x), __uint_as_float(v.y))
                       : attn::f2pack(__uint_as_float(v.z), __uint_as_float(v.w));
     }
-    __device__ static uint4 pack(const float (&f)[4]) {
+    __device__ static Raw pack(const float (&f)[V]) {
         return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
     }
 };
@@ -67,7 +71,7 @@ template <typename IOT, int W, bool SILU>
 __global__ void __launch_bounds__(kThreads)
 causal_conv_kernel(const ConvArgs a)
 {
-    constexpr int V = Vec<IOT>::n;
+    using Raw = typename Vec<IOT>::Raw;
     const int nvec = a.D / V;
     const int stretches = a.T > 0 ? (a.T - 1) / kStretch + 1 : 1;   // T = 0 carries the state over
     const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
@@ -81,9 +85,9 @@ causal_conv_kernel(const ConvArgs a)
 
     // the row of token t; tokens before the call come from the carried state
     auto row = [&](int t) {
-        if (t >= 0) return __ldg(reinterpret_cast<const uint4*>(x + t * a.x_row));
-        if (st) return *reinterpret_cast<const uint4*>(st + (long long)(t + W - 1) * a.D);
-        return make_uint4(0, 0, 0, 0);
+        if (t >= 0) return __ldg(reinterpret_cast<const Raw*>(x + t * a.x_row));
+        if (st) return *reinterpret_cast<const Raw*>(st + (long long)(t + W - 1) * a.D);
+        return Vec<IOT>::zero();
     };
 
     if (t0 < t1) {
@@ -98,14 +102,14 @@ causal_conv_kernel(const ConvArgs a)
         }
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
-            const uint4 v = row(t0 - (W - 1) + j);
+            const Raw v = row(t0 - (W - 1) + j);
 #pragma unroll
             for (int e = 0; e < V / 2; ++e) win[j][e] = Vec<IOT>::pair(v, e);
         }
         IOT* o = static_cast<IOT*>(a.out) + ((long long)b * a.T + t0) * a.D + c;
 #pragma unroll 1
         for (int t = t0; t < t1; t += kBatch) {
-            uint4 in[kBatch];
+            Raw in[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) in[i] = row(min(t + i, t1 - 1));
 #pragma unroll
@@ -127,18 +131,18 @@ causal_conv_kernel(const ConvArgs a)
                         r[2 * e + 1] = silu_f(r[2 * e + 1]);
                     }
                 }
-                if (t + i < t1) *reinterpret_cast<uint4*>(o) = Vec<IOT>::pack(r);
+                if (t + i < t1) *reinterpret_cast<Raw*>(o) = Vec<IOT>::pack(r);
                 o += a.D;
             }
         }
     }
     if (s == 0 && a.state_out) {
-        uint4 keep[W - 1];
+        Raw keep[W - 1];
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) keep[j] = row(n - (W - 1) + j);     // read before the state is written
         IOT* so = static_cast<IOT*>(a.state_out) + (long long)b * (W - 1) * a.D + c;
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) *reinterpret_cast<uint4*>(so + (long long)j * a.D) = keep[j];
+        for (int j = 0; j < W - 1; ++j) *reinterpret_cast<Raw*>(so + (long long)j * a.D) = keep[j];
     }
 }
 
@@ -155,7 +159,7 @@ template <typename IOT>
 cudaError_t launch_conv(const ConvArgs& a, int width, bool silu, cudaStream_t stream)
 {
     const int stretches = a.T > 0 ? (a.T - 1) / conv::kStretch + 1 : 1;
-    const long long items = (long long)(a.D / conv::Vec<IOT>::n) * stretches;
+    const long long items = (long long)(a.D / conv::V) * stretches;
     const long long blocks = (items + conv::kThreads - 1) / conv::kThreads;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)blocks, (unsigned)a.B);

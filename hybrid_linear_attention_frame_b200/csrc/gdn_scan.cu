@@ -11,7 +11,7 @@
 // threads that own the states.
 //
 // A CTA owns 16 channels of one batch entry.  Its four scan warps hold the states: 8 threads
-// share a channel, N / 8 states each.  Its four helper warps walk the same tokens a tile of 64
+// share a channel, N / 8 states each.  Its eight helper warps walk the same tokens a tile of 128
 // ahead: they read the rows with 16-byte loads (the next tile's into registers while this one
 // is worked on), put delta, delta x, B and C into shared memory, and later turn the scan's sums
 // into rows of y.  The two sides meet at named barriers, two buffers each way.
@@ -94,10 +94,10 @@ template <> struct Eight<float> {
 
 constexpr int kC = 16;                     // channels per CTA
 constexpr int kL = 8;                      // threads per channel
-constexpr int kTile = 64;                  // tokens per tile
-constexpr int kScanThreads = kC * kL;      // 128: warps 0-3; the helpers are warps 4-7
-constexpr int kThreads = 2 * kScanThreads;
-static_assert(kScanThreads == kTile * 2, "a helper thread has one token and 8 channels of a tile");
+constexpr int kTile = 128;                 // tokens per tile
+constexpr int kScanThreads = kC * kL;      // warps 0-3
+constexpr int kHelpers = 2 * kTile;        // warps 4-11: a helper has one token and 8 channels of a tile
+constexpr int kThreads = kScanThreads + kHelpers;
 constexpr int kDRow = kTile + 2;           // (delta, delta x) per channel, padded off the banks
 constexpr int kYRow = 20;                  // sums per token: 16 channels, padded so that 8 tokens x 4
                                            // channels, a warp's store, fall on 32 banks
@@ -214,11 +214,11 @@ template <int W> __device__ __forceinline__ void sum_round(float (&v)[8], int l)
 }
 
 template <typename IOT, int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, N <= 16 && sizeof(IOT) == 2 ? 2 : 1)
 selective_scan_kernel(const ScanArgs a)
 {
     constexpr int S = N / kL;
-    constexpr int kRing = S == 8 ? 2 : 4;                                // pairs of tokens
+    constexpr int kRing = 2;                                             // pairs of tokens
     extern __shared__ __align__(16) uint8_t smem[];
     float2* s_d = reinterpret_cast<float2*>(smem);                       // [2][kC][kDRow]
     float* s_bc = reinterpret_cast<float*>(s_d + 2 * kC * kDRow);        // [2][kTile][kL][B: S | C: S]
@@ -283,7 +283,7 @@ selective_scan_kernel(const ScanArgs a)
         const IOT* Bm = static_cast<const IOT*>(a.Bm) + b * a.b_batch;
         const IOT* Cm = static_cast<const IOT*>(a.Cm) + b * a.c_batch;
         IOT* y = static_cast<IOT*>(a.y) + (long long)b * a.T * a.D + c;
-        constexpr int kBC = (kTile * N / 8 + kScanThreads - 1) / kScanThreads;   // 8-state pieces of B (and C) a thread
+        constexpr int kBC = (kTile * N / 8 + kHelpers - 1) / kHelpers;   // 8-state pieces of B (and C) a thread
         float bias[8], skip[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -302,7 +302,7 @@ selective_scan_kernel(const ScanArgs a)
             }
 #pragma unroll
             for (int i = 0; i < kBC; ++i) {
-                const int p = tid + i * kScanThreads, pt = k * kTile + p / (N / 8), ps = 8 * (p % (N / 8));
+                const int p = tid + i * kHelpers, pt = k * kTile + p / (N / 8), ps = 8 * (p % (N / 8));
                 rb[i].zero(); rc[i].zero();
                 if (p < kTile * N / 8 && pt < n) {
                     rb[i].load(Bm + pt * a.b_row + ps);
@@ -342,7 +342,7 @@ selective_scan_kernel(const ScanArgs a)
             }
 #pragma unroll
             for (int i = 0; i < kBC; ++i) {
-                const int p = tid + i * kScanThreads;
+                const int p = tid + i * kHelpers;
                 if (p < kTile * N / 8) {
                     const int pt = p / (N / 8), pu = p % (N / 8);
                     float4* w = reinterpret_cast<float4*>(s_bc + (buf * kTile + pt) * 2 * N);
