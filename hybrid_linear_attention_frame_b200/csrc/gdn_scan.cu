@@ -35,12 +35,17 @@ struct ScanArgs {
 namespace scan {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2eLow = (float)(1.4426950408889634 - (double)kLog2e);
 
 // log(1 + e^x) = max(x, 0) + log1p(u), u = e^-|x| in (0, 1], through
 // log1p(u) = 2 artanh(s), s = u / (2 + u) <= 1/3, whose series s + s^3/3 + .. + s^13/13 leaves
-// out less than 2e-8 of the value: relative accuracy holds where softplus is tiny.
+// out less than 2e-8 of the value: relative accuracy holds where softplus is tiny.  There it is u
+// itself, whose exponent's rounding error (|x| 2^-24 of u) is taken along as `low`.
 __device__ __forceinline__ float softplus_series(float x) {
-    const float u = attn::ex2(-fabsf(x) * kLog2e);
+    const float e = -fabsf(x) * kLog2e;
+    const float low = fmaf(-fabsf(x), kLog2e, -e) - fabsf(x) * kLog2eLow;
+    float u = attn::ex2(e);
+    u = fmaf(u, low * 0.69314718f, u);
     const float s = __fdividef(u, 2.0f + u), q = s * s;
     float r = fmaf(q, 1.0f / 13.0f, 1.0f / 11.0f);
     r = fmaf(r, q, 1.0f / 9.0f);
@@ -59,6 +64,14 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 
 // v silu(g); the quotient of a gate far below 0 is 0
 __device__ __forceinline__ float gated(float v, float g) { return v * __fdividef(g, 1.0f + attn::ex2(-g * kLog2e)); }
+
+// Four consecutive elements of a row, 8- or 16-byte aligned.
+__device__ __forceinline__ float4 four(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ float4 four(const __nv_bfloat16* p) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xffff0000u));
+}
 
 // Eight consecutive elements of a row.
 template <typename IOT> struct Eight;
@@ -376,10 +389,12 @@ selective_scan_kernel(const ScanArgs a)
 }
 
 // The next token of every session: the states stream through once, so HBM bounds it (8 bytes
-// per state).  A thread has 4 states of one channel; N / 4 threads sum a channel's output.
-constexpr int kStepThreads = 256;
+// per state).  A thread has 4 states of one channel, in kMany sessions at once where there are enough
+// of them: their loads are in flight together, and A is read once for all.  N / 4 threads sum a
+// channel's output.
+constexpr int kStepThreads = 256, kMany = 4;
 
-template <typename IOT, int N>
+template <typename IOT, int N, int Sessions>
 __global__ void __launch_bounds__(kStepThreads)
 selective_scan_step_kernel(const ScanArgs a)
 {
@@ -388,29 +403,43 @@ selective_scan_step_kernel(const ScanArgs a)
     const int l = (int)(id % L);
     const long long ch = id / L;
     const bool live = ch < a.D;
-    const int c = live ? (int)ch : 0, b = blockIdx.y;
-    const float4 A = *reinterpret_cast<const float4*>(a.A + (long long)c * N + 4 * l);
-    const long long so = ((long long)b * a.D + c) * N + 4 * l;
-    float4 h = live ? *reinterpret_cast<const float4*>(a.state_in + so) : make_float4(0, 0, 0, 0);
-    const float x = to_f32(static_cast<const IOT*>(a.x)[b * a.x_batch + c]);
-    float de = to_f32(static_cast<const IOT*>(a.dt)[b * a.dt_batch + c]) + (a.dt_bias ? a.dt_bias[c] : 0.0f);
-    if (a.softplus) de = softplus_series(de);
-    const IOT* Bm = static_cast<const IOT*>(a.Bm) + b * a.b_batch + 4 * l;
-    const IOT* Cm = static_cast<const IOT*>(a.Cm) + b * a.c_batch + 4 * l;
-    const float dx = de * x, d2 = de * kLog2e;
-    h.x = fmaf(attn::ex2(d2 * A.x), h.x, dx * to_f32(Bm[0]));
-    h.y = fmaf(attn::ex2(d2 * A.y), h.y, dx * to_f32(Bm[1]));
-    h.z = fmaf(attn::ex2(d2 * A.z), h.z, dx * to_f32(Bm[2]));
-    h.w = fmaf(attn::ex2(d2 * A.w), h.w, dx * to_f32(Bm[3]));
-    float y = fmaf(h.x, to_f32(Cm[0]), fmaf(h.y, to_f32(Cm[1]), fmaf(h.z, to_f32(Cm[2]), h.w * to_f32(Cm[3]))));
+    const int c = live ? (int)ch : 0, b0 = blockIdx.y * Sessions;
+    const long long so = ((long long)b0 * a.D + c) * N + 4 * l, sb = (long long)a.D * N;
+    float4 h[Sessions];
+    float x[Sessions], de[Sessions], z[Sessions];
 #pragma unroll
-    for (int k = L / 2; k > 0; k >>= 1) y += __shfl_xor_sync(0xffffffffu, y, k);
-    if (!live) return;
-    *reinterpret_cast<float4*>(a.state_out + so) = h;
-    if (l == 0) {
-        if (a.skip) y = fmaf(a.skip[c], x, y);
-        if (a.z) y = gated(y, to_f32(static_cast<const IOT*>(a.z)[b * a.z_batch + c]));
-        static_cast<IOT*>(a.y)[(long long)b * a.D + c] = from_f32<IOT>(y);
+    for (int k = 0; k < Sessions; ++k) {
+        const int b = min(b0 + k, a.B - 1);                // (a session past the last: read, not written)
+        h[k] = *reinterpret_cast<const float4*>(a.state_in + so + (b - b0) * sb);
+        x[k] = to_f32(static_cast<const IOT*>(a.x)[b * a.x_batch + c]);
+        de[k] = to_f32(static_cast<const IOT*>(a.dt)[b * a.dt_batch + c]);
+        z[k] = a.z ? to_f32(static_cast<const IOT*>(a.z)[b * a.z_batch + c]) : 0.0f;
+    }
+    float4 A = *reinterpret_cast<const float4*>(a.A + (long long)c * N + 4 * l);
+    A.x *= kLog2e; A.y *= kLog2e; A.z *= kLog2e; A.w *= kLog2e;
+    const float bias = a.dt_bias ? a.dt_bias[c] : 0.0f, skip = a.skip ? a.skip[c] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < Sessions; ++k) {
+        const int b = min(b0 + k, a.B - 1);
+        const float4 B = four(static_cast<const IOT*>(a.Bm) + b * a.b_batch + 4 * l);
+        const float4 C = four(static_cast<const IOT*>(a.Cm) + b * a.c_batch + 4 * l);
+        float d = de[k] + bias;
+        if (a.softplus) d = softplus_series(d);
+        const float dx = d * x[k];
+        h[k].x = fmaf(attn::ex2(d * A.x), h[k].x, dx * B.x);
+        h[k].y = fmaf(attn::ex2(d * A.y), h[k].y, dx * B.y);
+        h[k].z = fmaf(attn::ex2(d * A.z), h[k].z, dx * B.z);
+        h[k].w = fmaf(attn::ex2(d * A.w), h[k].w, dx * B.w);
+        float y = fmaf(h[k].x, C.x, fmaf(h[k].y, C.y, fmaf(h[k].z, C.z, h[k].w * C.w)));
+#pragma unroll
+        for (int w = L / 2; w > 0; w >>= 1) y += __shfl_xor_sync(0xffffffffu, y, w);
+        if (!live || b0 + k >= a.B) continue;
+        *reinterpret_cast<float4*>(a.state_out + so + k * sb) = h[k];
+        if (l == 0) {
+            y = fmaf(skip, x[k], y);
+            if (a.z) y = gated(y, z[k]);
+            static_cast<IOT*>(a.y)[(long long)b * a.D + c] = from_f32<IOT>(y);
+        }
     }
 }
 
@@ -418,9 +447,18 @@ template <typename IOT, int N>
 cudaError_t launch(const ScanArgs& a, bool step, cudaStream_t stream)
 {
     if (step) {
+        int dev = 0, sms = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
         const long long threads = (long long)a.D * (N / 4);
-        const dim3 grid((unsigned)((threads + kStepThreads - 1) / kStepThreads), (unsigned)a.B);
-        selective_scan_step_kernel<IOT, N><<<grid, kStepThreads, 0, stream>>>(a);
+        const unsigned blocks = (unsigned)((threads + kStepThreads - 1) / kStepThreads);
+        // several sessions a thread as long as the threads still fill the device twice
+        if (threads * a.B >= 2 * 2048ll * kMany * sms)
+            selective_scan_step_kernel<IOT, N, kMany>
+                <<<dim3(blocks, (unsigned)((a.B + kMany - 1) / kMany)), kStepThreads, 0, stream>>>(a);
+        else
+            selective_scan_step_kernel<IOT, N, 1><<<dim3(blocks, (unsigned)a.B), kStepThreads, 0, stream>>>(a);
         return cudaGetLastError();
     }
     if (smem_bytes<N>() > 48 * 1024) {     // (a per-device setting of the current context: set on every call)

@@ -33,12 +33,15 @@ def softplus(x):
 
 
 def selective_scan(x, dt, A, Bm, Cm, skip=None, z=None, dt_bias=None, state=None, dt_softplus=True,
-                   arg_eps=2.0 ** -21, exp_eps=2.0 ** -22, add_eps=2.0 ** -23):
+                   arg_eps=2.0 ** -20, exp_eps=2.0 ** -22, add_eps=2.0 ** -23):
     """One sequence: x, dt, z [T, D], Bm, Cm [T, N], A and state [D, N].
 
     Returns y, the last state, and first-order bounds on what float32 arithmetic may add to each:
     exp(delta A) off by |delta A| arg_eps + exp_eps of its value, the two roundings of the update by
-    add_eps, carried along the recurrence.
+    add_eps, carried along the recurrence.  In units of 2^-24: an approximate exponential and a quotient
+    are off by 3 and 4, so softplus through u = e^-|x|, u / (2 + u) and its odd series is off by
+    3 + 1 + 4 for the quotient and 2 for the last products, 10 together, and delta A or delta x by 2
+    products more: 12, below 16 = arg_eps.
     """
     x, dt, A, Bm, Cm = (np.asarray(v, np.float64) for v in (x, dt, A, Bm, Cm))
     T, D = x.shape

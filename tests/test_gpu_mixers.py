@@ -239,7 +239,7 @@ def test_scan_pieces_and_steps(cuda, dtype, N):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
-@pytest.mark.parametrize("B,D,N", [(1, 8, 16), (7, 136, 8), (300, 24, 16), (3, 264, 32), (2, 72, 64)])
+@pytest.mark.parametrize("B,D,N", [(1, 8, 16), (7, 136, 8), (300, 24, 16), (301, 2240, 32), (3, 264, 32), (2, 72, 64)])
 def test_scan_step(cuda, dtype, B, D, N):
     g = gen(B + D)
     p = scan_inputs(g, B, 1, D, N, dtype)
