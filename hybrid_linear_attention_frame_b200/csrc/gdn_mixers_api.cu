@@ -43,7 +43,7 @@ bool overlaps_any(const void* p, size_t bytes, const Span (&s)[N])
 int run_conv(gdn::ConvArgs a, int width, int silu, size_t elem, cudaStream_t stream)
 {
     if (a.B < 1 || a.T < 0 || a.D < 1 || (silu != 0 && silu != 1)) return GDN_ERR_INVALID_ARG;
-    if (width < 2 || width > 4 || a.D % 8 || a.B > 65535) return GDN_ERR_UNSUPPORTED;
+    if (width < 2 || width > 4 || a.D % 8 || a.B > 65535 || a.T > INT32_MAX - 1024) return GDN_ERR_UNSUPPORTED;
     if (!a.weight || (a.T > 0 && (!a.x || !a.out))) return GDN_ERR_INVALID_ARG;
     if (!aligned(a.out, 16) || !aligned(a.state_in, 16) || !aligned(a.state_out, 16) || !aligned(a.weight, 4) ||
         !aligned(a.bias, 4) || !aligned(a.lengths, 4))
@@ -69,7 +69,8 @@ int run_conv(gdn::ConvArgs a, int width, int silu, size_t elem, cudaStream_t str
 int run_scan(gdn::ScanArgs a, int softplus, size_t elem, bool step, cudaStream_t stream)
 {
     if (a.B < 1 || a.T < 0 || a.D < 1 || a.N < 1 || (softplus != 0 && softplus != 1)) return GDN_ERR_INVALID_ARG;
-    if ((a.N != 8 && a.N != 16 && a.N != 32 && a.N != 64) || a.D % 8 || a.B > 65535) return GDN_ERR_UNSUPPORTED;
+    if ((a.N != 8 && a.N != 16 && a.N != 32 && a.N != 64) || a.D % 8 || a.B > 65535 || a.T > INT32_MAX - 1024)
+        return GDN_ERR_UNSUPPORTED;
     if (!a.A || (a.T > 0 && (!a.x || !a.dt || !a.Bm || !a.Cm || !a.y))) return GDN_ERR_INVALID_ARG;
     if (!aligned(a.y, 16) || !aligned(a.A, 16) || !aligned(a.state_in, 16) || !aligned(a.state_out, 16) ||
         !aligned(a.skip, 4) || !aligned(a.dt_bias, 4) || !aligned(a.lengths, 4))

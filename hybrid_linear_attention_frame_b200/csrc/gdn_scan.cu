@@ -15,6 +15,12 @@
 // ahead: they read the rows with 16-byte loads (the next tile's into registers while this one
 // is worked on), put delta, delta x, B and C into shared memory, and later turn the scan's sums
 // into rows of y.  The two sides meet at named barriers, two buffers each way.
+//
+// Where channels and batch entries leave SMs idle, the CTAs of a cluster cut the sequence between
+// them.  Each first runs its segment from a zero state without outputs, which gives the segment's
+// own end state E and the sum of its deltas (the segment decays what enters it by exp(A sum)); they
+// read each other's through distributed shared memory, so that each knows the state that enters its
+// segment, and the segments then run in full.  Twice the exponentials for up to 8 times the SMs.
 #include "gdn_common.cuh"
 #include "gdn_sm100.cuh"
 
@@ -117,7 +123,7 @@ constexpr int kYRow = 20;                  // sums per token: 16 channels, padde
 enum { kFull = 1, kEmpty = 3, kYFull = 5, kYEmpty = 7 };   // named barriers, + buffer
 
 template <int N> constexpr int smem_bytes() {
-    return 2 * (kC * kDRow * 8 + kTile * 2 * N * 4 + kTile * kYRow * 4);
+    return 2 * (kC * kDRow * 8 + kTile * 2 * N * 4 + kTile * kYRow * 4) + (kC * N + kC) * 4;
 }
 
 __device__ __forceinline__ void bar_arrive(int id) {
@@ -204,6 +210,21 @@ template <int S> struct States {
         attn::f2unpack(s, s0, s1);
         return s0 + s1;
     }
+    __device__ void clear() {
+#pragma unroll
+        for (int i = 0; i < P; ++i) h[i] = 0ull;
+    }
+    // a whole segment: its sum of deltas and its own end state
+    __device__ void pass(float sum, const float (&end)[S]) {
+        float a0, a1, h0, h1;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int j = S > 1 ? 2 * i + 1 : 0;
+            attn::f2unpack(A[i], a0, a1);
+            attn::f2unpack(h[i], h0, h1);
+            h[i] = attn::f2pack(fmaf(attn::ex2(sum * a0), h0, end[2 * i]), fmaf(attn::ex2(sum * a1), h1, end[j]));
+        }
+    }
     __device__ void store(float* o) const {
         float a, b;
 #pragma unroll
@@ -226,19 +247,30 @@ template <int W> __device__ __forceinline__ void sum_round(float (&v)[8], int l)
     }
 }
 
-template <typename IOT, int N>
-__global__ void __launch_bounds__(kThreads, N <= 16 && sizeof(IOT) == 2 ? 2 : 1)
+// CTAs that an SM holds: two in 80 registers a thread where that loses nothing.
+template <typename IOT, int N> constexpr int resident() { return N <= 16 && sizeof(IOT) == 2 ? 2 : 1; }
+
+// Cut: the clusters' CTAs share a sequence (a kernel of its own, since the uncut one is slower by 9 %
+// with that code beside it).
+template <typename IOT, int N, bool Cut>
+__global__ void __launch_bounds__(kThreads, resident<IOT, N>())
 selective_scan_kernel(const ScanArgs a)
 {
     constexpr int S = N / kL;
+    static_assert(kL == 8 && kC * kL == kScanThreads, "thread l of a channel");
     constexpr int kRing = 2;                                             // pairs of tokens
     extern __shared__ __align__(16) uint8_t smem[];
     float2* s_d = reinterpret_cast<float2*>(smem);                       // [2][kC][kDRow]
     float* s_bc = reinterpret_cast<float*>(s_d + 2 * kC * kDRow);        // [2][kTile][kL][B: S | C: S]
     float* s_y = s_bc + 2 * kTile * 2 * N;                               // [2][kTile][kYRow]
-    const int b = blockIdx.y, c0 = blockIdx.x * kC;
-    const int n = a.lengths ? min(max(a.lengths[b], 0), a.T) : a.T;
-    const int tiles = (n + kTile - 1) / kTile;
+    float* s_end = s_y + 2 * kTile * kYRow;                              // [kC][N] end states, [kC] sums of delta
+    const int X = Cut ? (int)sm100::cluster_size() : 1, rank = Cut ? (int)sm100::cluster_rank() : 0;
+    const int b = blockIdx.y, c0 = (int)(blockIdx.x / (unsigned)X) * kC;
+    const int len = a.lengths ? min(max(a.lengths[b], 0), a.T) : a.T;
+    // this CTA's segment: tokens t0 .. n - 1
+    const int seg = ((len + X - 1) / X + kTile - 1) / kTile * kTile;
+    const int t0 = Cut ? min(rank * seg, len) : 0, n = Cut ? min(t0 + seg, len) : len;
+    const int tiles = (n - t0 + kTile - 1) / kTile;
 
     if (threadIdx.x < kScanThreads) {
         // ======================= the states =======================
@@ -247,6 +279,50 @@ selective_scan_kernel(const ScanArgs a)
         States<S> s;
         const long long so = ((long long)b * a.D + c) * N + l * S;
         s.init(live ? a.A + (long long)c * N + l * S : nullptr, (live && a.state_in) ? a.state_in + so : nullptr);
+        if constexpr (Cut) {
+            const States<S> enter = s;
+            s.clear();
+            float sum = 0.0f, lost = 0.0f;                               // of delta, compensated
+            for (int k = 0; k < tiles; ++k) {
+                const int buf = k & 1;
+                const uint32_t d = sm100::smem_u32(s_d + (buf * kC + ch) * kDRow);
+                const uint32_t bc = sm100::smem_u32(s_bc + buf * kTile * 2 * N);
+                bar_sync(kFull + buf);
+                Tokens<S> ring[kRing];
+#pragma unroll
+                for (int u = 0; u < kRing - 1; ++u) ring[u].load(d + 16 * u, bc + 16 * N * u, 2 * u, l);
+                const int groups = (min(kTile, n - t0 - k * kTile) + 7) / 8;
+#pragma unroll 1
+                for (int g = 0; g < groups; ++g) {
+                    float part = 0.0f;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int ahead = u + kRing - 1;
+                        ring[ahead % kRing].load(d + 16 * (4 * g + ahead), bc + 16 * N * (4 * g + ahead), 2 * ahead & 7, l);
+                        const Tokens<S>& now = ring[u % kRing];
+                        part += now.de[0] + now.de[1];
+                        (void)s.step(now, 0);
+                        (void)s.step(now, 1);
+                    }
+                    const float add = part - lost, next = sum + add;
+                    lost = (next - sum) - add;
+                    sum = next;
+                }
+                if (k + 2 < tiles) bar_arrive(kEmpty + buf);
+            }
+            s.store(s_end + ch * N + l * S);
+            if (l == 0) s_end[kC * N + ch] = sum;
+            sm100::cluster_sync();
+            s = enter;
+            const uint32_t end = sm100::smem_u32(s_end);
+            for (int r = 0; r < rank; ++r) {
+                float e[S];
+#pragma unroll
+                for (int i = 0; i < S; ++i) e[i] = sm100::ld_remote(end + 4 * (ch * N + l * S + i), r);
+                s.pass(sm100::ld_remote(end + 4 * (kC * N + ch), r), e);
+            }
+            sm100::cluster_sync();                                              // no one reads s_end any more
+        }
         for (int k = 0; k < tiles; ++k) {
             const int buf = k & 1;
             const uint32_t d = sm100::smem_u32(s_d + (buf * kC + ch) * kDRow);
@@ -259,7 +335,7 @@ selective_scan_kernel(const ScanArgs a)
             Tokens<S> ring[kRing];
 #pragma unroll
             for (int u = 0; u < kRing - 1; ++u) ring[u].load(d + 16 * u, bc + 16 * N * u, 2 * u, l);
-            const int groups = (min(kTile, n - k * kTile) + 7) / 8;
+            const int groups = (min(kTile, n - t0 - k * kTile) + 7) / 8;
             float last[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll 1
             for (int g = 0; g < groups; ++g) {
@@ -285,7 +361,7 @@ selective_scan_kernel(const ScanArgs a)
             bar_arrive(kYFull + buf);
             if (k + 2 < tiles) bar_arrive(kEmpty + buf);
         }
-        if (live && a.state_out) s.store(a.state_out + so);
+        if (live && a.state_out && rank == X - 1) s.store(a.state_out + so);
     } else {
         // ======================= rows in, rows out =======================
         const int tid = threadIdx.x - kScanThreads, row = tid >> 1, cv = 8 * (tid & 1), c = c0 + cv;
@@ -305,7 +381,7 @@ selective_scan_kernel(const ScanArgs a)
         }
         Eight<IOT> rx, rd, rz, px, pz, rb[kBC], rc[kBC];
         auto fetch = [&](int k) {
-            const int t = k * kTile + row;
+            const int t = t0 + k * kTile + row;
             const bool on = live && t < n;
             rx.zero(); rd.zero(); rz.zero();
             if (on) {
@@ -315,7 +391,7 @@ selective_scan_kernel(const ScanArgs a)
             }
 #pragma unroll
             for (int i = 0; i < kBC; ++i) {
-                const int p = tid + i * kHelpers, pt = k * kTile + p / (N / 8), ps = 8 * (p % (N / 8));
+                const int p = tid + i * kHelpers, pt = t0 + k * kTile + p / (N / 8), ps = 8 * (p % (N / 8));
                 rb[i].zero(); rc[i].zero();
                 if (p < kTile * N / 8 && pt < n) {
                     rb[i].load(Bm + pt * a.b_row + ps);
@@ -324,7 +400,7 @@ selective_scan_kernel(const ScanArgs a)
             }
         };
         auto finish = [&](int k, const Eight<IOT>& fx, const Eight<IOT>& fz) {
-            const int buf = k & 1, t = k * kTile + row;
+            const int buf = k & 1, t = t0 + k * kTile + row;
             bar_sync(kYFull + buf);
             float f[8];
             const float4* v = reinterpret_cast<const float4*>(s_y + (buf * kTile + row) * kYRow + cv);
@@ -339,10 +415,9 @@ selective_scan_kernel(const ScanArgs a)
             }
             if (live && t < n) Eight<IOT>::store(y + (long long)t * a.D, f);
         };
-        if (tiles > 0) fetch(0);
-        for (int k = 0; k < tiles; ++k) {
+        auto produce = [&](int k) {
             const int buf = k & 1;
-            const bool on = live && k * kTile + row < n;
+            const bool on = live && t0 + k * kTile + row < n;
             if (k >= 2) bar_sync(kEmpty + buf);
             // padding leaves the state as it is: delta = 0, and B = C = 0 from fetch
             float2* d = s_d + (buf * kC + cv) * kDRow + row;
@@ -378,6 +453,19 @@ selective_scan_kernel(const ScanArgs a)
                 }
             }
             bar_arrive(kFull + buf);
+        };
+        if constexpr (Cut) {
+            if (tiles > 0) fetch(0);
+            for (int k = 0; k < tiles; ++k) {
+                produce(k);
+                if (k + 1 < tiles) fetch(k + 1);
+            }
+            sm100::cluster_sync();
+            sm100::cluster_sync();
+        }
+        if (tiles > 0) fetch(0);
+        for (int k = 0; k < tiles; ++k) {
+            produce(k);
             const Eight<IOT> cx = rx, cz = rz;
             if (k + 1 < tiles) fetch(k + 1);
             if (k > 0) finish(k - 1, px, pz);
@@ -461,14 +549,38 @@ cudaError_t launch(const ScanArgs& a, bool step, cudaStream_t stream)
             selective_scan_step_kernel<IOT, N, 1><<<dim3(blocks, (unsigned)a.B), kStepThreads, 0, stream>>>(a);
         return cudaGetLastError();
     }
+    // Sequences are cut in 4 or 8 while all CTAs are resident at once and a segment has a tile; in 2 it
+    // does not pay.  8192 tokens of N = 16: 64 CTAs 211 us whole, 147 us in 4; 32 CTAs 210 us whole, 90 us
+    // in 4, 75 us in 8; 94 CTAs, beyond the rule, 213 us whole and 218 us in 4.
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const long long blocks = (a.D + kC - 1) / kC, ctas = blocks * a.B;
+    int X = 8;
+    while (X > 2 && (ctas * X > (long long)resident<IOT, N>() * sms || a.T < kTile * X)) X /= 2;
+    if (X == 2) X = 1;
+    auto kernel = X > 1 ? selective_scan_kernel<IOT, N, true> : selective_scan_kernel<IOT, N, false>;
     if (smem_bytes<N>() > 48 * 1024) {     // (a per-device setting of the current context: set on every call)
-        const cudaError_t e = cudaFuncSetAttribute(selective_scan_kernel<IOT, N>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<N>());
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<N>());
         if (e != cudaSuccess) return e;
     }
-    const dim3 grid((unsigned)((a.D + kC - 1) / kC), (unsigned)a.B);
-    selective_scan_kernel<IOT, N><<<grid, kThreads, smem_bytes<N>(), stream>>>(a);
-    return cudaGetLastError();
+    if (X == 1) {
+        kernel<<<dim3((unsigned)blocks, (unsigned)a.B), kThreads, smem_bytes<N>(), stream>>>(a);
+        return cudaGetLastError();
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks * X), (unsigned)a.B);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes<N>();
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)X;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace scan

@@ -166,6 +166,9 @@ def check_scan(p, n, y, h, dtype, what, softplus=True):
 @pytest.mark.parametrize("B,T,D,N,lengths", [
     (1, 1, 8, 16, None), (2, 3, 24, 8, None), (1, 31, 40, 32, None), (1, 32, 16, 64, None), (2, 33, 136, 16, [33, 7]),
     (4, 65, 72, 16, [0, 1, 64, 65]), (1, 300, 264, 16, None), (1, 257, 48, 64, None), (5, 100, 200, 8, [3, 100, 50, 99, 32]),
+    # long enough that a cluster shares a sequence, also one that leaves some of its blocks without tokens
+    (1, 512, 24, 16, None), (1, 1025, 8, 16, None), (2, 1100, 40, 8, [1100, 130]), (2, 600, 16, 32, [600, 0]),
+    (1, 1300, 24, 64, None),
 ])
 def test_scan(cuda, dtype, B, T, D, N, lengths):
     g = gen(T * 7 + N)
