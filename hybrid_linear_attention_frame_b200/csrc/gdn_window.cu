@@ -256,13 +256,35 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tmem_alloc(base + kOffTmemSlot, kTmemCols);
         tmem_relinquish();
     }
-    if (tid == 32) {
-        for (uint32_t i = 0; i < kNumBars; ++i) mbar_init(bar(i), bar_count(i));
-        fence_mbar_init();
-        *abort_flag = 0;
+    auto load_k = [&](int j) {
+        const uint32_t s = (uint32_t)(j % kKStages), full = bar(kBarKFull + s);
+        mbar_arrive_expect_tx(full, (uint32_t)nbk * kBox);
+        for (int c = 0; c < nbk; ++c)
+            tma_load_4d(base + kOffK + s * kOp + c * kBox, &tm_k, full, 64 * c, p.head[0] / a.group, p.start(j), b);
+    };
+    auto load_v = [&](int j) {
+        const uint32_t s = (uint32_t)(j % kVStages), full = bar(kBarVFull + s);
+        mbar_arrive_expect_tx(full, (uint32_t)nbv * kBox);
+        for (int c = 0; c < nbv; ++c)
+            tma_load_4d(base + kOffV + s * kOp + c * kBox, &tm_v, full, 64 * c, p.head[0] / a.group, p.start(j), b);
+    };
+    if (warp == kLoadWarp && lane == 0) {
+        // the first copies start beside the allocation
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
+        for (uint32_t i = 0; i < kNumBars; ++i) mbar_init(bar(i), bar_count(i));
+        fence_mbar_init();
+        *abort_flag = 0;
+        const uint32_t live = (p.p_hi[0] >= p.p_lo[0] ? 1u : 0u) + (p.p_hi[1] >= p.p_lo[1] ? 1u : 0u);
+        mbar_arrive_expect_tx(bar(kBarQ), live * (uint32_t)nbk * kBox);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            if (p.p_hi[q] >= p.p_lo[q])
+                for (int c = 0; c < nbk; ++c)
+                    tma_load_4d(base + kOffQ + q * kOp + c * kBox, &tm_q, bar(kBarQ), 64 * c, p.head[q], p.row0[q], b);
+        load_k(0);
+        load_v(0);
         tma_prefetch_desc(&tm_o);
     }
     tc_fence_before();
@@ -272,31 +294,19 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
     if (warp == kLoadWarp) {
         // ======================= copies =======================
-        const int hk = p.head[0] / a.group;
-        bool ok = true;
-        int k_issued = 0, v_issued = 0;
         if (lane == 0) {
-            const uint32_t live = (p.p_hi[0] >= p.p_lo[0] ? 1u : 0u) + (p.p_hi[1] >= p.p_lo[1] ? 1u : 0u);
-            mbar_arrive_expect_tx(bar(kBarQ), live * (uint32_t)nbk * kBox);
-            for (int q = 0; q < 2; ++q)
-                if (p.p_hi[q] >= p.p_lo[q])
-                    for (int c = 0; c < nbk; ++c)
-                        tma_load_4d(base + kOffQ + q * kOp + c * kBox, &tm_q, bar(kBarQ), 64 * c, p.head[q], p.row0[q], b);
-            for (int j = 0; ok && j < p.n; ++j) {
-                const int sk = j % kKStages, sv = j % kVStages;
+            bool ok = true;
+            int k_issued = 1, v_issued = 1;
+            for (int j = 1; ok && j < p.n; ++j) {
                 if (j >= kKStages)
-                    ok = mbar_wait(bar(kBarKFree + sk), (uint32_t)((j / kKStages - 1) & 1), abort_flag, lim, 41);
+                    ok = mbar_wait(bar(kBarKFree + j % kKStages), (uint32_t)((j / kKStages - 1) & 1), abort_flag, lim, 41);
                 if (!ok) break;
-                mbar_arrive_expect_tx(bar(kBarKFull + sk), (uint32_t)nbk * kBox);
-                for (int c = 0; c < nbk; ++c)
-                    tma_load_4d(base + kOffK + sk * kOp + c * kBox, &tm_k, bar(kBarKFull + sk), 64 * c, hk, p.start(j), b);
+                load_k(j);
                 k_issued = j + 1;
                 if (j >= kVStages)
-                    ok = mbar_wait(bar(kBarVFree + sv), (uint32_t)((j / kVStages - 1) & 1), abort_flag, lim, 42);
+                    ok = mbar_wait(bar(kBarVFree + j % kVStages), (uint32_t)((j / kVStages - 1) & 1), abort_flag, lim, 42);
                 if (!ok) break;
-                mbar_arrive_expect_tx(bar(kBarVFull + sv), (uint32_t)nbv * kBox);
-                for (int c = 0; c < nbv; ++c)
-                    tma_load_4d(base + kOffV + sv * kOp + c * kBox, &tm_v, bar(kBarVFull + sv), 64 * c, hk, p.start(j), b);
+                load_v(j);
                 v_issued = j + 1;
             }
             // copies land before shared memory goes away, whoever gave up: the last one of each stage is
@@ -676,7 +686,11 @@ window_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const uint32_t bars = smem_u32(smem) + tail + 8u * kStages * warp;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + tail + 8u * kStages * kWarps);
     if (lane < kStages) mbar_init(bars + 8u * lane, 1);
-    if (tid == 0) *abort_flag = 0;
+    if (tid == 0) {
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+        *abort_flag = 0;
+    }
     fence_mbar_init();
     __syncthreads();
     if (pos < 0) return;                       // idle: the whole cluster leaves
