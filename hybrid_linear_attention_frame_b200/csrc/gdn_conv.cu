@@ -95,14 +95,17 @@ causal_conv_kernel(const ConvArgs a)
 
     if (t0 < t1) {
         uint64_t w[W][V / 2], bias[V / 2], win[W - 1][V / 2];
+        alignas(16) float wf[V * W];                                  // 4 W consecutive floats
 #pragma unroll
-        for (int e = 0; e < V / 2; ++e) {
-            bias[e] = a.bias ? attn::f2pack(__ldg(a.bias + c + 2 * e), __ldg(a.bias + c + 2 * e + 1)) : 0ull;
+        for (int i = 0; i < W; ++i)
+            *reinterpret_cast<float4*>(wf + 4 * i) = __ldg(reinterpret_cast<const float4*>(a.weight + (long long)c * W) + i);
+        const float4 bf = a.bias ? __ldg(reinterpret_cast<const float4*>(a.bias + c)) : make_float4(0, 0, 0, 0);
+        bias[0] = attn::f2pack(bf.x, bf.y);
+        bias[1] = attn::f2pack(bf.z, bf.w);
 #pragma unroll
-            for (int j = 0; j < W; ++j)
-                w[j][e] = attn::f2pack(__ldg(a.weight + (long long)(c + 2 * e) * W + j),
-                                       __ldg(a.weight + (long long)(c + 2 * e + 1) * W + j));
-        }
+        for (int e = 0; e < V / 2; ++e)
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][e] = attn::f2pack(wf[2 * e * W + j], wf[(2 * e + 1) * W + j]);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
             const Raw v = row(t0 - (W - 1) + j);

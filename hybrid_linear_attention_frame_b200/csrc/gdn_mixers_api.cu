@@ -45,8 +45,8 @@ int run_conv(gdn::ConvArgs a, int width, int silu, size_t elem, cudaStream_t str
     if (a.B < 1 || a.T < 0 || a.D < 1 || (silu != 0 && silu != 1)) return GDN_ERR_INVALID_ARG;
     if (width < 2 || width > 4 || a.D % 8 || a.B > 65535 || a.T > INT32_MAX - 1024) return GDN_ERR_UNSUPPORTED;
     if (!a.weight || (a.T > 0 && (!a.x || !a.out))) return GDN_ERR_INVALID_ARG;
-    if (!aligned(a.out, 16) || !aligned(a.state_in, 16) || !aligned(a.state_out, 16) || !aligned(a.weight, 4) ||
-        !aligned(a.bias, 4) || !aligned(a.lengths, 4))
+    if (!aligned(a.out, 16) || !aligned(a.state_in, 16) || !aligned(a.state_out, 16) || !aligned(a.weight, 16) ||
+        !aligned(a.bias, 16) || !aligned(a.lengths, 4))
         return GDN_ERR_INVALID_ARG;
     Rows x{a.x, a.x_batch, a.x_row};
     size_t nx = 0;

@@ -34,7 +34,7 @@ CONV = dict(x=at(1), xb=64 * 32, xr=32, weight=at(2), bias=at(3), state_in=at(4)
     (dict(x=None), INV), (dict(weight=None), INV), (dict(out=None), INV), (dict(B=0), INV), (dict(T=-1), INV),
     (dict(D=0), INV), (dict(silu=2), INV), (dict(width=1), UNS), (dict(width=5), UNS), (dict(D=12), UNS),
     (dict(B=65536), UNS), (dict(x=at(1) + 8), INV), (dict(out=at(7) + 4), INV), (dict(state_in=at(4) + 8), INV),
-    (dict(lengths=at(6) + 2), INV), (dict(xr=31), INV), (dict(xr=33), INV), (dict(xb=-64), INV),
+    (dict(lengths=at(6) + 2), INV), (dict(weight=at(2) + 4), INV), (dict(bias=at(3) + 8), INV), (dict(xr=31), INV), (dict(xr=33), INV), (dict(xb=-64), INV),
     (dict(xr=1 << 60), INV), (dict(out=at(1) + 64), INV), (dict(out=at(4)), INV), (dict(out=at(5)), INV),
     (dict(state_out=at(1)), INV), (dict(state_out=at(4) + 16), INV), (dict(state_out=at(2)), INV),
 ])
