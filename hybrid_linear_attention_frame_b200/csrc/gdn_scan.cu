@@ -16,6 +16,10 @@
 // is worked on), put delta, delta x, B and C into shared memory, and later turn the scan's sums
 // into rows of y.  The two sides meet at named barriers, two buffers each way.
 //
+// A step of one CTA's 16 channels (N = 16) takes 20 clocks of the special-function unit and about 27 of
+// shared memory (loads and shuffles); one CTA alone on an SM needs 45, two 38 each.  27,280 tokens of
+// 2240 channels: 660 us, 1.5 T exponentials a second; N = 64: 2.4 T.
+//
 // Where channels and batch entries leave SMs idle, the CTAs of a cluster cut the sequence between
 // them.  Each first runs its segment from a zero state without outputs, which gives the segment's
 // own end state E and the sum of its deltas (the segment decays what enters it by exp(A sum)); they

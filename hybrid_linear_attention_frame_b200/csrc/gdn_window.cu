@@ -69,18 +69,25 @@ bool make_map(CUtensorMap* map, const void* ptr, int d, int H, long long T, int 
 // One CTA per pair of 128-query tiles (two query heads that share a key head where there are
 // such, else two tiles of consecutive queries), which read the same K and V tiles:
 //   S_q = Q_q K^T on the tensor cores into TMEM, q = 0, 1;
-//   softmax of tile q by its own four warps, one thread per query row, against a reference m, the
+//   softmax of tile q by its own eight warps, two threads per query row, against a reference m, the
 //     row's largest score in its first tile: it moves only when a tile's weights sum to more than
 //     2^30, so later tiles need no maximum and O is hardly ever rescaled (the division by the
 //     running sum at the end is right for any m);
 //   P in bf16 over the score columns it came from, O_q += P_q V with P as the A operand.
-// S and P of a query tile have two buffers of 64 keys (P over the scores that it came from), the
-// halves of a 128-key tile.  Warp 8 issues, half by half, PV_0(j-1) S_0(j) PV_1(j-1) S_1(j); the
-// tensor cores execute in order, so S(j) may overwrite P(j-1) of its half, and while a softmax
-// weighs one half, the other half's next scores are on their way.
-// Warp 9 keeps K (3 stages) and V (2 stages) coming by TMA.  Key tiles are counted from the
-// window's first key, sink tiles before them when the two do not touch, so no key is visited
-// twice; a tile that a query tile sees nothing of is skipped for it.  Every wait is bounded.
+// S and P of a query tile have two buffers of 64 keys, the halves of a 128-key tile and one thread of
+// each row.  Warp 16 issues, half by half, PV_0(j-1) S_0(j) PV_1(j-1) S_1(j); the tensor cores execute
+// in order, so S(j) may overwrite P(j-1) of its half, and while a softmax weighs one half, the other
+// half's products run.  Warp 17 keeps K (3 stages) and V (2 stages) coming by TMA.  Key tiles are
+// counted from the window's first key, sink tiles before them when the two do not touch, so no key is
+// visited twice; a tile that a query tile sees nothing of is skipped for it.  Every wait is bounded.
+//
+// A step (two query tiles, 128 keys, d 128) needs 2.0 K cycles of the tensor cores and 1.8 K of the
+// special-function unit; it takes about 3.6 K, the two taking turns at each buffer.  27,280 tokens,
+// 20 heads on 4, d 128, window 2640 + 880 sinks: 892 us, 1,031 TFLOP/s; causal over 8192 tokens, 32
+// heads on 8: 499 us, 1,101 TFLOP/s.  What the form rests on: one thread per row weighing 128 keys held
+// the chain from scores to weights to scores at 4.2 K cycles; with S and P in one buffer per tile the
+// softmax waited for both products; an issuing thread that sleeps at its barriers adds 300 cycles to
+// every hand-off (1,008 against 972 us).
 namespace tc {
 
 using namespace sm100;
@@ -204,6 +211,7 @@ __device__ __forceinline__ Plan make_plan(const Args& a, int n_keys) {
 }
 
 __device__ __forceinline__ uint64_t kmaj(uint32_t addr) { return smem_desc(addr, 16, 1024, kSwizzle128); }
+
 // The issuing thread's wait: polls without suspending (a suspended thread takes ~300 cycles to resume,
 // which here would stand between a softmax and its next scores), bounded like every wait.
 __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns,
