@@ -8,8 +8,10 @@
 // 2 W + 5 operations and two special functions (the SiLU) per element against two elements of
 // traffic: bound by HBM, with the special-function unit busy for 0.7 of that time, so loads and
 // arithmetic have to overlap.  A thread owns 4 channels, few enough that 6 to 8 blocks of 128 threads
-// share an SM (8 channels a thread: 206 us against 108 us), and walks a stretch of tokens with the last W - 1 rows in registers; x is read once but
-// for the W - 1 rows of halo per stretch, and the loads of 8 rows are issued before the first is used.  Channels are the fastest thread index, so a warp reads and writes whole lines of a row.
+// share an SM (8 channels a thread: 206 us against 108 us), and walks a stretch of tokens with the
+// last W - 1 rows in registers; x is read once but for the W - 1 rows of halo per stretch, and the
+// loads of 8 rows are issued before the first is used.  Channels are the fastest thread index, so a
+// warp reads and writes whole lines of a row.
 // 27,280 tokens of 4480 channels, width 4, bf16: 100 us, 4.9 TB/s.
 #include "gdn_common.cuh"
 #include "gdn_sm100.cuh"
