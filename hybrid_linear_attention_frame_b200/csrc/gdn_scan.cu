@@ -50,10 +50,13 @@ constexpr float kLog2eLow = (float)(1.4426950408889634 - (double)kLog2e);
 // log(1 + e^x) = max(x, 0) + log1p(u), u = e^-|x| in (0, 1], through
 // log1p(u) = 2 artanh(s), s = u / (2 + u) <= 1/3, whose series s + s^3/3 + .. + s^13/13 leaves
 // out less than 2e-8 of the value: relative accuracy holds where softplus is tiny.  There it is u
-// itself, whose exponent's rounding error (|x| 2^-24 of u) is taken along as `low`.
+// itself, whose exponent's rounding error (|x| 2^-24 of u) is taken along as `low`.  u is 0 in float
+// from |x| = 104 on; the bound keeps e finite there, since low would be inf - inf: the lowest value
+// of a type and -inf, which mask a token, give 0.  (A select, so that NaN stays NaN.)
 __device__ __forceinline__ float softplus_series(float x) {
-    const float e = -fabsf(x) * kLog2e;
-    const float low = fmaf(-fabsf(x), kLog2e, -e) - fabsf(x) * kLog2eLow;
+    const float ax = fabsf(x) > 200.0f ? 200.0f : fabsf(x);
+    const float e = -ax * kLog2e;
+    const float low = fmaf(-ax, kLog2e, -e) - ax * kLog2eLow;
     float u = attn::ex2(e);
     u = fmaf(u, low * 0.69314718f, u);
     const float s = __fdividef(u, 2.0f + u), q = s * s;

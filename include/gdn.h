@@ -410,7 +410,8 @@ int gdn_causal_conv_step_f32(const float* x, long long x_batch_stride, const flo
  *              sequence's last valid token, or NULL; may be state_in
  * N = 8, 16, 32 or 64; D a multiple of 8.  The state and all sums are fp32; y is
  * rounded once.  T = 0 carries the state over.  gdn_selective_scan_step: T = 1,
- * the state in place.
+ * the state in place.  A dt of the type's lowest value or -inf masks a token (with
+ * dt_softplus): delta is 0, so the state stays as it is.
  */
 int gdn_selective_scan(const void* x, long long x_batch_stride, long long x_row_stride,
                        const void* dt, long long dt_batch_stride, long long dt_row_stride,

@@ -1,0 +1,80 @@
+"""The token-by-token mixers on values at the ends of the number range: masks by the type's lowest
+value or an infinity, growing and infinite states, NaN and infinities in tokens that a query does not
+see, sums that could overflow, idle sessions; and that a call repeats itself bit for bit.
+
+Compared with the float64 oracle under the tolerances of test_gpu_mixers.py; where the oracle's value
+is not finite, the kernel's has to be the same infinity or NaN.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import hybrid_linear_attention_frame_b200 as G
+from oracle import mixers_reference as M
+from test_gpu_mixers import (HALF, TYPES, Guarded, assert_near, attn_inputs, attn_tol, check_scan, done, gen, ids, normal,
+                             np64, scan_inputs)
+
+pytestmark = pytest.mark.gpu
+
+INF, NAN = float("inf"), float("nan")
+
+
+def same_kind(got, ref, tol, what):
+    """Finite values within the tolerance, the others alike."""
+    on = np.isfinite(ref)
+    assert np.array_equal(got[~on], ref[~on], equal_nan=True), f"{what}: infinities and NaN differ"
+    assert_near(got[on], ref[on], tol[on], what)
+
+
+def run_scan(p, form, softplus=True, lengths=None):
+    """A scan in one of its forms: tokens at once ("prompt"; "cut" where a cluster shares the sequence) or
+    one at a time; y [B, T, D] and the last state in 64 bits."""
+    if form == "step":
+        h, y = p["state"].clone(), []
+        for t in range(p["x"].shape[1]):
+            s = {k: None if p[k] is None else p[k][:, t] for k in ("x", "dt", "z", "Bm", "Cm")}
+            y.append(G.selective_scan_step(s["x"], s["dt"], p["A"], s["Bm"], s["Cm"], h, p["D"], s["z"], p["dt_bias"],
+                                           softplus))
+        y = torch.stack(y, 1)
+    else:
+        y, h = G.selective_scan(p["x"], p["dt"], p["A"], p["Bm"], p["Cm"], p["D"], p["z"], p["dt_bias"], p["state"],
+                                softplus, lengths)
+    done()
+    return np64(y), np64(h)
+
+
+TOKENS = {"prompt": 21, "cut": 1100, "step": 5}
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("form", ["prompt", "cut", "step"])
+def test_scan_masks_by_the_lowest_value(cuda, dtype, form):
+    """softplus of the lowest value of a type and of -inf is 0, so such a token leaves the state as it is;
+    above, softplus is its argument (here with x = 0, which empties the state)."""
+    g = gen(101)
+    T = TOKENS[form]
+    p = scan_inputs(g, 1, T, 16, 16, dtype)
+    p["dt_bias"] = None
+    low = torch.finfo(dtype).min
+    for c, v in enumerate((low, -INF, -2.37e38)):
+        p["dt"][0, :, c] = v                          # every token masked
+        p["dt"][0, 1::3, 4 + c] = v                   # some
+    if form != "cut":
+        p["dt"][0, 2, 8], p["x"][0, 2, 8] = -low, 0.0
+        p["dt"][0, 3, 9], p["x"][0, 3, 9] = 2.37e38, 0.0
+    y, h = run_scan(p, form)
+    check_scan(p, [T], y, h, dtype, f"masked scan, {form}")
+    assert np.array_equal(h[0, :3], np64(p["state"][0, :3]))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("form", ["prompt", "step"])
+def test_scan_keeps_nan_steps(cuda, dtype, form):
+    """A NaN step is the caller's to see: its channel becomes NaN, no other one."""
+    g = gen(103)
+    p = scan_inputs(g, 1, 5, 16, 16, dtype)
+    p["dt"][0, 1, 3] = NAN
+    y, h = run_scan(p, form)
+    assert np.isnan(h[0, 3]).all() and np.isnan(y[0, 1:, 3]).all()
+    assert np.isfinite(np.delete(h[0], 3, 0)).all() and np.isfinite(np.delete(y[0], 3, 1)).all()
