@@ -81,7 +81,8 @@ __device__ __forceinline__ float gated(float v, float g) { return v * __fdividef
 // One state over one token in the float32 mode, e^x h + b.  The hardware's exponential reads low by 1e-8
 // to 3e-8 on average below 0, which a memory of a thousand tokens sums up to a hundred roundings; so for
 // |x| <= 1/8 the result is h + ((e^x - 1) h + b) with the Taylor polynomial of e^x - 1 (what it leaves out
-// is below 5e-8 of itself).  Beyond that a memory is short.
+// is below 5e-8 of itself).  Beyond that a memory is short; and an infinite h, where the difference form
+// is inf - inf, takes the plain one too.
 __device__ __forceinline__ float exact_step(float x, float h, float b) {
     float p = fmaf(x, 1.0f / 120.0f, 1.0f / 24.0f);
     p = fmaf(p, x, 1.0f / 6.0f);
@@ -89,8 +90,9 @@ __device__ __forceinline__ float exact_step(float x, float h, float b) {
     p = fmaf(p, x, 1.0f) * x;
     const float near = h + fmaf(p, h, b), far = fmaf(attn::ex2(x * kLog2e), h, b);
     float r;                               // a select, not a branch: lanes differ (47 us against 20 us, 3 x 517 tokens)
-    asm("{\n\t.reg .pred q;\n\tsetp.le.f32 q, %1, 0f3e000000;\n\tselp.f32 %0, %2, %3, q;\n\t}"
-        : "=f"(r) : "f"(fabsf(x)), "f"(near), "f"(far));
+    asm("{\n\t.reg .pred q;\n\tsetp.le.f32 q, %1, 0f3e000000;\n\tsetp.lt.and.f32 q, %4, 0f7f800000, q;\n\t"
+        "selp.f32 %0, %2, %3, q;\n\t}"
+        : "=f"(r) : "f"(fabsf(x)), "f"(near), "f"(far), "f"(fabsf(h)));
     return r;
 }
 

@@ -78,3 +78,40 @@ def test_scan_keeps_nan_steps(cuda, dtype, form):
     y, h = run_scan(p, form)
     assert np.isnan(h[0, 3]).all() and np.isnan(y[0, 1:, 3]).all()
     assert np.isfinite(np.delete(h[0], 3, 0)).all() and np.isfinite(np.delete(y[0], 3, 1)).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("form,lengths", [("prompt", None), ("prompt", [13, 21]), ("step", None)])
+def test_scan_keeps_an_infinite_state(cuda, dtype, form, lengths):
+    """exp(.) inf + . is inf, also through small and zero steps and through the padding of a group of tokens."""
+    g = gen(104)
+    T = TOKENS[form]
+    p = scan_inputs(g, 2, T, 16, 8, dtype)
+    p["A"].clamp_(min=-2)                             # (no decay that underflows)
+    n = [T, T] if lengths is None else lengths
+    p["dt"][:, 1] = torch.finfo(dtype).min if dtype == torch.float32 else -200.0
+    p["state"][0, 2, 3], p["state"][1, 5, 0] = INF, -INF
+    ln = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device=cuda)
+    y, h = run_scan(p, form, lengths=ln)
+    for b, c, s in ((0, 2, 3), (1, 5, 0)):
+        assert h[b, c, s] == np64(p["state"])[b, c, s]
+        sign = np.sign(np64(p["Cm"][b, :n[b], s]) * np64(p["z"][b, :n[b], c])) * h[b, c, s]
+        assert np.array_equal(y[b, :n[b], c], sign)
+        p["state"][b, c] = 0.0                        # the channel's other states, and everything else: the oracle
+        y[b, :, c], h[b, c] = 0.0, 0.0
+        p["x"][b, :, c] = 0.0
+    check_scan(p, n, y, h, dtype, f"infinite states, {form}")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("form", ["prompt", "step"])
+def test_scan_of_an_infinite_step_is_infinite(cuda, dtype, form):
+    g = gen(102)
+    p = scan_inputs(g, 1, 5, 16, 16, dtype)
+    p["dt_bias"] = None
+    p["A"].clamp_(min=-2)                             # (no decay that underflows)
+    p["dt"][0, 1, 3] = INF
+    _, h = run_scan(p, form)
+    want = np.sign(np64(p["x"][0, 1, 3]) * np64(p["Bm"][0, 1])) * INF
+    assert np.array_equal(h[0, 3], want)
+    assert np.isfinite(np.delete(h[0], 3, 0)).all()
