@@ -75,6 +75,13 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return d;
 }
 
+// A within the finite floats (NaN as it is), so that a step of 0 times it is 0 also where the decay is
+// unbounded: padding and masked tokens leave the state as it is, any other step forgets all of it.
+__device__ __forceinline__ float finite_rate(float a) {
+    constexpr float kTop = 3.4028235e38f;
+    return a < -kTop ? -kTop : a > kTop ? kTop : a;
+}
+
 // v silu(g); the quotient of a gate far below 0 is 0
 __device__ __forceinline__ float gated(float v, float g) { return v * __fdividef(g, 1.0f + attn::ex2(-g * kLog2e)); }
 
@@ -209,7 +216,7 @@ template <int S, bool Exact> struct States {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int j = S > 1 ? 2 * i + 1 : 0;
-            A[i] = a ? attn::f2pack(a[2 * i] * kUnit, a[j] * kUnit) : 0ull;
+            A[i] = a ? attn::f2pack(finite_rate(a[2 * i] * kUnit), finite_rate(a[j] * kUnit)) : 0ull;
             h[i] = h0 ? attn::f2pack(h0[2 * i], h0[j]) : 0ull;
         }
     }
@@ -538,6 +545,7 @@ selective_scan_step_kernel(const ScanArgs a)
         z[k] = a.z ? to_f32(static_cast<const IOT*>(a.z)[b * a.z_batch + c]) : 0.0f;
     }
     float4 A = *reinterpret_cast<const float4*>(a.A + (long long)c * N + 4 * l);
+    A = make_float4(finite_rate(A.x), finite_rate(A.y), finite_rate(A.z), finite_rate(A.w));
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.0f, skip = a.skip ? a.skip[c] : 0.0f;
 #pragma unroll
     for (int k = 0; k < Sessions; ++k) {

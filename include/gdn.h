@@ -404,7 +404,8 @@ int gdn_causal_conv_step_f32(const float* x, long long x_batch_stride, const flo
  *     y_t     = (sum_n Cm_t[n] h_t[n] + skip[d] x_t) silu(z_t).
  *   x, dt, z   [B, T, D] through strides (z may be NULL: no gate); y [B, T, D]
  *   Bm, Cm     [B, T, N] through strides, shared by all channels
- *   A          [D, N] float32, as it stands in the exponent (usually negative)
+ *   A          [D, N] float32, as it stands in the exponent (usually negative; -inf
+ *              forgets the state at every token with a step)
  *   skip, dt_bias   [D] float32 or NULL (0)
  *   state_in   [B, D, N] float32 or NULL (zeros); state_out the state after each
  *              sequence's last valid token, or NULL; may be state_in

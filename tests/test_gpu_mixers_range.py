@@ -115,3 +115,18 @@ def test_scan_of_an_infinite_step_is_infinite(cuda, dtype, form):
     want = np.sign(np64(p["x"][0, 1, 3]) * np64(p["Bm"][0, 1])) * INF
     assert np.array_equal(h[0, 3], want)
     assert np.isfinite(np.delete(h[0], 3, 0)).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("form", ["prompt", "cut", "step"])
+def test_scan_of_an_unbounded_decay(cuda, dtype, form):
+    """A = -inf forgets at every token with a step, and keeps the state where there is none: padding, masks."""
+    g = gen(105)
+    T = TOKENS[form]
+    p = scan_inputs(g, 2, T, 16, 8, dtype)
+    n = [T, T - 2] if form != "step" else [T, T]
+    p["dt"][0, T // 2, 4] = -INF                      # a masked token
+    p["A"][4, 2], p["A"][5, 0], p["A"][6, 1] = -INF, torch.finfo(torch.float32).min, -3e38
+    y, h = run_scan(p, form, lengths=None if form == "step" else torch.tensor(n, dtype=torch.int32, device=cuda))
+    p["A"][4, 2] = p["A"][5, 0] = p["A"][6, 1] = -1e30   # (as good, and finite times the oracle's zero steps)
+    check_scan(p, n, y, h, dtype, f"unbounded decay, {form}")
