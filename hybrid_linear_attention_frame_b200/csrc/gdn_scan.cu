@@ -254,6 +254,12 @@ template <int S, bool Exact> struct States {
 #pragma unroll
         for (int i = 0; i < P; ++i) h[i] = 0ull;
     }
+    // One state over a whole segment, e^x h + end.  The recurrence keeps a zero (or infinite) state as it is
+    // however much the segment grows (or shrinks) it; with the factor of the whole segment that would be 0 inf.
+    __device__ static float over(float x, float h, float end) {
+        const float r = Exact ? exact_step(x, h, end) : fmaf(attn::ex2(x), h, end);
+        return (h == 0.0f || fabsf(h) == INFINITY) ? h + end : r;
+    }
     // a whole segment: its sum of deltas and its own end state
     __device__ void pass(float sum, const float (&end)[S]) {
         float a0, a1, h0, h1;
@@ -262,8 +268,7 @@ template <int S, bool Exact> struct States {
             const int j = S > 1 ? 2 * i + 1 : 0;
             attn::f2unpack(A[i], a0, a1);
             attn::f2unpack(h[i], h0, h1);
-            if constexpr (Exact) h[i] = attn::f2pack(exact_step(sum * a0, h0, end[2 * i]), exact_step(sum * a1, h1, end[j]));
-            else h[i] = attn::f2pack(fmaf(attn::ex2(sum * a0), h0, end[2 * i]), fmaf(attn::ex2(sum * a1), h1, end[j]));
+            h[i] = attn::f2pack(over(sum * a0, h0, end[2 * i]), over(sum * a1, h1, end[j]));
         }
     }
     __device__ void store(float* o) const {

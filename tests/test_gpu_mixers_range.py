@@ -130,3 +130,33 @@ def test_scan_of_an_unbounded_decay(cuda, dtype, form):
     y, h = run_scan(p, form, lengths=None if form == "step" else torch.tensor(n, dtype=torch.int32, device=cuda))
     p["A"][4, 2] = p["A"][5, 0] = p["A"][6, 1] = -1e30   # (as good, and finite times the oracle's zero steps)
     check_scan(p, n, y, h, dtype, f"unbounded decay, {form}")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("T", [40, 600, 1100])
+def test_scan_growth_of_nothing_is_nothing(cuda, dtype, T):
+    """A growing channel whose inputs begin late stays 0 until then, however much a segment would grow it."""
+    g = gen(106)
+    p = scan_inputs(g, 1, T, 8, 16, dtype)
+    p["state"], p["dt_bias"] = None, None
+    p["A"][:, :4] = 0.5
+    p["dt"][:] = 1.0
+    p["x"][:, :T - 20] = 0.0
+    y, h = run_scan(p, "prompt", softplus=False)
+    check_scan(p, [T], y, h, dtype, "late growth", softplus=False)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("T", [40, 600, 1100])
+def test_scan_decay_of_infinity_is_infinity(cuda, dtype, T):
+    """An infinite state stays infinite however much a segment decays it."""
+    g = gen(108)
+    p = scan_inputs(g, 1, T, 8, 16, dtype)
+    p["dt_bias"] = None
+    p["A"].clamp_(min=-2)                             # (no step of the recurrence underflows)
+    p["dt"][:] = 1.0
+    p["state"][0, 1, 4] = -INF
+    _, h = run_scan(p, "prompt", softplus=False)
+    assert h[0, 1, 4] == -INF
+    h[0, 1, 4] = 0.0
+    assert np.isfinite(h).all()
