@@ -75,9 +75,9 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return d;
 }
 
-// A within the finite floats (NaN as it is), so that a step of 0 times it is 0 also where the decay is
-// unbounded: padding and masked tokens leave the state as it is, any other step forgets all of it.
-__device__ __forceinline__ float finite_rate(float a) {
+// a within the finite floats (NaN as it is).  Of A, so that a step of 0 times it is 0 also where the decay
+// is unbounded: padding and masked tokens leave the state as it is, any other step forgets all of it.
+__device__ __forceinline__ float clamp_finite(float a) {
     constexpr float kTop = 3.4028235e38f;
     return a < -kTop ? -kTop : a > kTop ? kTop : a;
 }
@@ -216,7 +216,7 @@ template <int S, bool Exact> struct States {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int j = S > 1 ? 2 * i + 1 : 0;
-            A[i] = a ? attn::f2pack(finite_rate(a[2 * i] * kUnit), finite_rate(a[j] * kUnit)) : 0ull;
+            A[i] = a ? attn::f2pack(clamp_finite(a[2 * i] * kUnit), clamp_finite(a[j] * kUnit)) : 0ull;
             h[i] = h0 ? attn::f2pack(h0[2 * i], h0[j]) : 0ull;
         }
     }
@@ -351,11 +351,12 @@ selective_scan_kernel(const ScanArgs a)
                         (void)s.step(now, 1);
                     }
                     const float add = part - lost, next = sum + add;
-                    lost = (next - sum) - add;
+                    lost = fabsf(next) < INFINITY ? (next - sum) - add : 0.0f;  // (of a sum past the range: nothing)
                     sum = next;
                 }
                 if (k + 2 < tiles) bar_arrive(kEmpty + buf);
             }
+            sum = clamp_finite(sum);                                             // (A = 0 keeps the state all the same)
             s.store(s_end + ch * N + l * S);
             if (l == 0) s_end[kC * N + ch] = sum;
             sm100::cluster_sync();
@@ -550,7 +551,7 @@ selective_scan_step_kernel(const ScanArgs a)
         z[k] = a.z ? to_f32(static_cast<const IOT*>(a.z)[b * a.z_batch + c]) : 0.0f;
     }
     float4 A = *reinterpret_cast<const float4*>(a.A + (long long)c * N + 4 * l);
-    A = make_float4(finite_rate(A.x), finite_rate(A.y), finite_rate(A.z), finite_rate(A.w));
+    A = make_float4(clamp_finite(A.x), clamp_finite(A.y), clamp_finite(A.z), clamp_finite(A.w));
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.0f, skip = a.skip ? a.skip[c] : 0.0f;
 #pragma unroll
     for (int k = 0; k < Sessions; ++k) {

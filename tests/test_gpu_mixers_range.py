@@ -160,3 +160,18 @@ def test_scan_decay_of_infinity_is_infinity(cuda, dtype, T):
     assert h[0, 1, 4] == -INF
     h[0, 1, 4] = 0.0
     assert np.isfinite(h).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("T", [600, 1100])
+def test_scan_with_steps_that_sum_past_the_range(cuda, dtype, T):
+    """Steps of the largest value (with x = 0: the state is emptied), several in a segment and in a group of tokens."""
+    g = gen(107)
+    p = scan_inputs(g, 1, T, 8, 16, dtype)
+    p["dt_bias"] = None
+    p["A"][:, 3] = 0.0                                # keeps its state whatever the step
+    top = torch.finfo(dtype).max
+    for c, at in enumerate(([3, 300, 301], [0, 1], [500], [130, 260, 390])):
+        p["dt"][0, at, c], p["x"][0, at, c] = top, 0.0
+    y, h = run_scan(p, "prompt")
+    check_scan(p, [T], y, h, dtype, "largest steps")
