@@ -810,9 +810,11 @@ window_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             mt[r] = fmaxf(mt[r], __shfl_xor_sync(0xffffffffu, mt[r], 1));
             mt[r] = fmaxf(mt[r], __shfl_xor_sync(0xffffffffu, mt[r], 2));
         }
-        const float mn[2] = {fmaxf(m[0], mt[0]), fmaxf(m[1], mt[1])};      // finite: a tile has a slot
+        // -inf as long as every score was; then the weights are 0, against a reference of 0
+        const float mn[2] = {fmaxf(m[0], mt[0]), fmaxf(m[1], mt[1])};
         if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
-            const float f[2] = {attn::ex2(m[0] - mn[0]), attn::ex2(m[1] - mn[1])};
+            const float f[2] = {mn[0] == -INFINITY ? 1.0f : attn::ex2(m[0] - mn[0]),
+                                mn[1] == -INFINITY ? 1.0f : attn::ex2(m[1] - mn[1])};
             l[0] *= f[0];
             l[1] *= f[1];
 #pragma unroll
@@ -824,11 +826,12 @@ window_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
         // P as A fragments (the layout of S as it is), split into a bf16 value and its remainder
         uint32_t ph[4], pl[4];
+        const float ref[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const float p0 = attn::ex2(s[h][2 * r] - m[r]), p1 = attn::ex2(s[h][2 * r + 1] - m[r]);
+                const float p0 = attn::ex2(s[h][2 * r] - ref[r]), p1 = attn::ex2(s[h][2 * r + 1] - ref[r]);
                 l[r] += p0 + p1;
                 const uint32_t hi = pack_bf16x2(p0, p1);
                 ph[2 * h + r] = hi;

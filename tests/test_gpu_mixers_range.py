@@ -175,3 +175,49 @@ def test_scan_with_steps_that_sum_past_the_range(cuda, dtype, T):
         p["dt"][0, at, c], p["x"][0, at, c] = top, 0.0
     y, h = run_scan(p, "prompt")
     check_scan(p, [T], y, h, dtype, "largest steps")
+
+
+def step_inputs(g, B, Hq, Hkv, d, window, sinks, pos):
+    t, cap = torch.bfloat16, window + sinks
+    q, k, v = normal(g, B, Hq, d, dtype=t), normal(g, B, Hkv, d, dtype=t), normal(g, B, Hkv, d, dtype=t)
+    kc, vc = normal(g, B, cap, Hkv, d, dtype=t), normal(g, B, cap, Hkv, d, dtype=t)
+    return q, k, v, kc, vc, torch.tensor(pos, dtype=torch.int32, device="cuda")
+
+
+def check_step(q, kc, vc, pos, out, window, sinks, what):
+    for i, p in enumerate(pos.tolist()):
+        m = min(window + sinks, p + 1)
+        with np.errstate(invalid="ignore"):
+            ref, mag = M.window_attention(np64(q[i])[None], np64(kc[i, :m]), np64(vc[i, :m]), m)
+        same_kind(out[i], ref[0], attn_tol(ref, mag)[0], f"{what}[{i}]")
+
+
+@pytest.mark.parametrize("value", [-INF, torch.finfo(torch.bfloat16).min])
+@pytest.mark.parametrize("Hq,Hkv,window,sinks", [(4, 2, 880, 16), (40, 2, 100, 0), (2, 2, 70, 5)])
+def test_window_step_with_keys_of_minus_infinity(cuda, value, Hq, Hkv, window, sinks):
+    """Keys whose score is -inf weigh nothing, also where they are all that a warp or a block has; a row that
+    sees no others is NaN, as the formula is."""
+    g = gen(110)
+    cap = window + sinks
+    q, k, v, kc, vc, pos = step_inputs(g, 5, Hq, Hkv, 64, window, sinks, [cap - 1, 3 * cap, cap // 2, cap + 40, 20])
+    q[..., 7] = 2.0
+    kc[0, :cap // 2, :, 7] = value                    # the first half of the slots
+    kc[1, 16:32, :, 7] = value                        # one tile
+    kc[2, 5:, :, 7] = value                           # the later ones; the new token's is finite
+    kc[3, :, :, 7] = value                            # all but the new token
+    kc[4, :, :, 7], k[4, :, 7] = value, value         # all
+    out = G.window_attention_step(q, k, v, kc, vc, pos, window, sinks)
+    done()
+    check_step(q, kc, vc, pos, np64(out), window, sinks, "step with -inf keys") if value == -INF else \
+        check_step(q[:4], kc[:4], vc[:4], pos[:4], np64(out)[:4], window, sinks, "step with the lowest keys")
+
+
+@pytest.mark.parametrize("pos", [15, 16, 17, 31, 32, 100])
+def test_window_step_shows_a_nan_key(cuda, pos):
+    """A NaN key that a position sees makes its heads' outputs NaN, wherever its slot lies."""
+    g = gen(111)
+    q, k, v, kc, vc, p = step_inputs(g, 2, 4, 2, 64, 90, 10, [pos, pos])
+    k[0, 1, 3] = NAN
+    out = G.window_attention_step(q, k, v, kc, vc, p, 90, 10)
+    done()
+    assert torch.isnan(out[0, 2:]).all() and torch.isfinite(out[0, :2]).all() and torch.isfinite(out[1]).all()
