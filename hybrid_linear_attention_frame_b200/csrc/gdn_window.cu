@@ -69,10 +69,12 @@ bool make_map(CUtensorMap* map, const void* ptr, int d, int H, long long T, int 
 // One CTA per pair of 128-query tiles (two query heads that share a key head where there are
 // such, else two tiles of consecutive queries), which read the same K and V tiles:
 //   S_q = Q_q K^T on the tensor cores into TMEM, q = 0, 1;
-//   softmax of tile q by its own eight warps, two threads per query row, against a reference m, the
-//     row's largest score in its first tile: it moves only when a tile's weights sum to more than
-//     2^30, so later tiles need no maximum and O is hardly ever rescaled (the division by the
-//     running sum at the end is right for any m);
+//   softmax of tile q by its own eight warps, two threads per query row, against a reference m, 16 (in
+//     powers of 2) above the row's largest score in its first tile: it moves only when a thread's 64
+//     weights of a tile sum to more than 64, so later tiles need no maximum and O is hardly ever
+//     rescaled (the division by the running sum at the end is right for any m).  So no sum is larger
+//     than if every weight were at most 1, and the 2^-16 that O may be small by is within what float
+//     has below bf16's smallest values;
 //   P in bf16 over the score columns it came from, O_q += P_q V with P as the A operand.
 // S and P of a query tile have two buffers of 64 keys, the halves of a 128-key tile and one thread of
 // each row.  Warp 16 issues, half by half, PV_0(j-1) S_0(j) PV_1(j-1) S_1(j); the tensor cores execute
@@ -122,7 +124,9 @@ constexpr uint32_t kSmemBytes = kOffM + 2u * kBM * 4u + 1024u;   // + slack for 
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;     // + 128 q each; S: two buffers of 64 columns
-constexpr float kMaxSum = 1073741824.0f;       // of a row's weights in a tile, before its reference moves
+// The reference lies kAbove over the largest score that it was taken from, and moves when a thread's 64
+// weights sum to more than kMaxSum: scores may rise by 2^16 at least (one alone by 2^22) before it does.
+constexpr float kAbove = 16.0f, kMaxSum = 64.0f;
 constexpr uint32_t kIdS = idesc_bf16(128, 64, false, false);
 
 struct Args {
@@ -466,8 +470,8 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
                 return true;
             };
-            // the row's largest score among this thread's columns
-            auto largest = [&]() {
+            // a reference for the row: above the largest score among this thread's columns
+            auto above = [&]() {
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -478,14 +482,14 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
                     for (int e = 0; e < 16; ++e) mx[e & 3] = attn::max3f(mx[e & 3], x[2 * e], x[2 * e + 1]);
                 }
-                return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+                return fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), a.scale_log2, kAbove);
             };
             // Moves the references up to it, and O along, once it is complete up to here.
             auto look_up = [&]() {
                 const bool none = half == 0 && i == 0;        // no P V yet
                 if (!none && !wait(bar(kBarH + 2 * q + (half ^ 1)), (uint32_t)(half ? i : i - 1), 50)) return false;
                 tc_fence_after();
-                const float mn = fmaxf(m_ref, largest());
+                const float mn = fmaxf(m_ref, above());
                 const float alpha = mn > m_ref ? attn::ex2(m_ref - mn) : 1.0f;
                 l *= alpha;
                 m_ref = mn;
@@ -507,7 +511,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (!wait(bar_s, (uint32_t)i, 47)) break;
             tc_fence_after();
             if (i == 0) {
-                m_ref = largest();
+                m_ref = above();
                 if (!swap([&](float other) { m_ref = fmaxf(m_ref, other); return m_ref; }, m_ref, 0)) break;
                 settled = !__any_sync(0xffffffffu, m_ref == -INFINITY);
             } else if (!settled) {
@@ -515,8 +519,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (__any_sync(0xffffffffu, m_ref == -INFINITY) && !look_up()) break;
                 settled = !__any_sync(0xffffffffu, m_ref == -INFINITY);
             }
-            // 2^(x scale - m) without looking for the maximum first: m is a score of an earlier tile, and
-            // float and bf16 hold what is 2^30 times as large as well as what is as large.
+            // 2^(x scale - m) without looking for the maximum first: m is above a score of an earlier tile.
             uint32_t pk[32];
             float sum;
             bool looked = !settled;

@@ -221,3 +221,42 @@ def test_window_step_shows_a_nan_key(cuda, pos):
     out = G.window_attention_step(q, k, v, kc, vc, p, 90, 10)
     done()
     assert torch.isnan(out[0, 2:]).all() and torch.isfinite(out[0, :2]).all() and torch.isfinite(out[1]).all()
+
+
+@pytest.mark.parametrize("value", [-INF, torch.finfo(torch.bfloat16).min])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (4, 2)])
+def test_window_attention_with_keys_of_minus_infinity(cuda, value, Hq, Hkv):
+    """Whole key tiles, a sink and single tokens with scores of -inf; queries that see no others are NaN."""
+    g = gen(112)
+    T, window, sinks = 500, 140, 3
+    q, k, v = attn_inputs(g, 1, T, T, Hq, Hkv, 64, 64)
+    q[..., 7] = 2.0
+    for s in (slice(100, 300), 400):
+        k[0, s, :, 7] = value
+    if value == -INF:
+        k[0, :3, :, 7] = value                        # all sinks: queries 239 to 299 see nothing else
+    o = np64(G.window_attention(q, k, v, window, sinks))
+    done()
+    with np.errstate(invalid="ignore"):
+        ref, mag = M.window_attention(np64(q[0]), np64(k[0]), np64(v[0]), window, sinks)
+    assert np.isnan(ref).any() == (value == -INF)
+    same_kind(o[0], ref, attn_tol(ref, mag), "prompt with -inf keys")
+
+
+@pytest.mark.parametrize("size", [1e30, 1e35, 1e-30, 1e-37])
+@pytest.mark.parametrize("rise", [0.0, 10.0, 14.0, 20.0, 40.0])
+def test_window_attention_over_the_range_of_values(cuda, size, rise):
+    """Values near the ends of bf16's range, and scores that rise by `rise` (base e) from tile to tile: no sum
+    overflows on the way, and small values are not lost.  (2^-133 is bf16's smallest step.)"""
+    g = gen(113)
+    T, d = 600, 64
+    q, k, v = attn_inputs(g, 1, T, T, 2, 1, d, d, std=0.5)
+    v = (v.float() * size).to(torch.bfloat16)
+    q[..., 0] = 8.0                                   # its score is the key's first element
+    k[0, :, 0, 0] = torch.arange(T, device=cuda).div(128, rounding_mode="floor").to(torch.bfloat16) * rise
+    o = np64(G.window_attention(q, k, v, 400, 4))
+    done()
+    ref, mag = M.window_attention(np64(q[0]), np64(k[0]), np64(v[0]), 400, 4)
+    S = 8.0 * 4 * rise / 8.0 + 8.0
+    tol = 2.0 ** -8 * (np.abs(ref) + mag) + (2.0 ** -12 + 2 * S * 2.0 ** -20) * mag + 4 * 2.0 ** -133
+    assert_near(o[0], ref, tol, "values at the ends of the range")
