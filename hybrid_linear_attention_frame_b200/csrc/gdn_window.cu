@@ -130,6 +130,8 @@ constexpr float kAbove = 16.0f, kMaxSum = 64.0f;
 constexpr uint32_t kIdS = idesc_bf16(128, 64, false, false);
 
 struct Args {
+    const __nv_bfloat16 *q, *k, *v;            // (as the tensor maps have them; for the rows that are done again)
+    long long q_batch, q_row, q_head, k_batch, k_row, k_head, v_batch, v_row, v_head;
     const int* lengths;
     __nv_bfloat16* out;
     int Tq, Tk, Hq, group, dk, dv, window, sinks;
@@ -179,12 +181,12 @@ struct Plan {
     __device__ bool active(int q, int j) const { return j < first_end[q] || (j >= near[q] && j < end[q]); }
 };
 
-__device__ __forceinline__ Plan make_plan(const Args& a, int n_keys) {
+__device__ __forceinline__ Plan make_plan(const Args& a, int n_keys, uint32_t block) {
     Plan p;
     const int off = a.Tk - a.Tq;
     // later queries see more: their blocks come first
-    const int rb = a.row_blocks - 1 - (int)(blockIdx.x / (unsigned)a.head_blocks);
-    const int hb = (int)(blockIdx.x % (unsigned)a.head_blocks);
+    const int rb = a.row_blocks - 1 - (int)(block / (uint32_t)a.head_blocks);
+    const int hb = (int)(block % (uint32_t)a.head_blocks);
     int lo = INT32_MAX, hi = -1;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -246,9 +248,100 @@ __device__ __forceinline__ void mma_bf16_tmem_a(uint32_t d_tmem, uint32_t a_tmem
                  : "memory");
 }
 
+// The weights of tokens that a row does not see are 0, and 0 times an infinity or NaN in their values is NaN:
+// on the tensor cores such a token of a visited tile reaches rows that it must not.  So a warp that wrote a NaN
+// does again, key by key in f32, those of its 32 rows (64 columns) that have such a token beside what they see.
+// The tokens that row t's query tile visits and that t does not see lie in [min(sink, t + 1), ws) from the
+// window's first tile on, and in (t, end of the last tile).
+__device__ __forceinline__ void redo_rows(const Args& a) {
+    // (Everything anew, the plan too: kept in the kernel's registers for this, or in a function of its own, it
+    // costs calls that never come here 5 %: 43.9 us instead of 41.2 for 2640 tokens, window 880.)
+    uint32_t block, tid;
+    int b;
+    asm volatile("mov.u32 %0, %%ctaid.x;\n\tmov.u32 %1, %%ctaid.y;\n\tmov.u32 %2, %%tid.x;" : "=r"(block), "=r"(b), "=r"(tid));
+    const int warp = (int)tid >> 5, lane = tid & 31, q_tile = warp / kTileWarps, half = (warp >> 2) & 1;
+    const int n_keys = a.lengths ? min(max(a.lengths[b], 0), a.Tk) : a.Tk, cols = min(64, a.dv - 64 * half);
+    const Plan p = make_plan(a, n_keys, block);
+    const int head = p.head[q_tile], t0 = p.p_lo[q_tile] + 32 * (warp & 3), live = min(32, p.p_hi[q_tile] + 1 - t0);
+    if (live <= 0 || cols <= 0) return;
+    const int near_key = p.startB > 0 || p.nA > 0 ? p.start(p.near[q_tile]) : 0;
+    const int end = min(n_keys, p.start(p.end[q_tile] - 1) + kBN), off = a.Tk - a.Tq;
+    if (lane == 0) bulk_wait_group0();         // the warp's rows are out before any is written again
+    __syncwarp();
+    const __nv_bfloat16* k = a.k + b * a.k_batch + head / a.group * a.k_head;
+    const __nv_bfloat16* v = a.v + b * a.v_batch + head / a.group * a.v_head + 64 * half;
+    for (int t = t0; t < t0 + live; ++t) {
+        const int i = t - off, ws = max(0, t - a.window + 1);
+        // four tokens at a time: is there one?
+        bool hit = false;
+        for (int part = 0; part < 2 && !hit; ++part) {
+            const int lo = part ? t + 1 : max(min(p.sink, t + 1), near_key), hi = part ? end : ws;
+            for (int s0 = lo; s0 < hi && !hit; s0 += 4) {
+                const int s = s0 + (lane >> 3), c = 8 * (lane & 7);
+                bool bad = false;
+                if (s < hi && c < cols) {
+                    const uint4 w = __ldg(reinterpret_cast<const uint4*>(v + s * a.v_row + c));
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        bad |= (u[e] & 0x7f80u) == 0x7f80u || (u[e] & 0x7f800000u) == 0x7f800000u;
+                }
+                hit = __any_sync(0xffffffffu, bad);
+            }
+        }
+        if (!hit) continue;
+        const uint4* q = reinterpret_cast<const uint4*>(a.q + b * a.q_batch + i * a.q_row + head * a.q_head);
+        float m = -INFINITY, l = 0.0f, o0 = 0.0f, o1 = 0.0f;      // l: this lane's keys; o: columns 2 lane, 2 lane + 1
+        bool whole = true;                     // (until every column is NaN)
+        for (int part = 0; part < 2; ++part) {
+            const int lo = part ? ws : 0, hi = part ? t + 1 : min(p.sink, ws);
+            for (int s0 = lo; s0 < hi && whole; s0 += 32) {
+                float x = -INFINITY;
+                if (s0 + lane < hi) {          // a lane's key
+                    const uint4* kq = reinterpret_cast<const uint4*>(k + (s0 + lane) * a.k_row);
+                    x = 0.0f;
+                    for (int c = 0; c < a.dk / 8; ++c) {
+                        const uint4 w = __ldg(kq + c), g = __ldg(q + c);
+                        const uint32_t u[4] = {w.x, w.y, w.z, w.w}, h[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x = fmaf(__uint_as_float(u[e] << 16), __uint_as_float(h[e] << 16), x);
+                            x = fmaf(__uint_as_float(u[e] & 0xffff0000u), __uint_as_float(h[e] & 0xffff0000u), x);
+                        }
+                    }
+                    x *= a.scale_log2;
+                }
+                float mn = x;
+                for (int w = 16; w > 0; w >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, w));
+                mn = fmaxf(m, mn);
+                const float f = mn > m ? attn::ex2(m - mn) : 1.0f, pr = attn::ex2(x - (mn == -INFINITY ? 0.0f : mn));
+                m = mn;
+                l = fmaf(l, f, pr);
+                o0 *= f;
+                o1 *= f;
+                const int n = min(32, hi - s0);
+                for (int j = 0; j < n; ++j) {
+                    const float w = __shfl_sync(0xffffffffu, pr, j);
+                    if (2 * lane < cols) {
+                        const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(v + (s0 + j) * a.v_row) + lane);
+                        o0 = fmaf(w, __uint_as_float(u << 16), o0);
+                        o1 = fmaf(w, __uint_as_float(u & 0xffff0000u), o1);
+                    }
+                }
+                whole = !__all_sync(0xffffffffu, 2 * lane >= cols || (isnan(o0) && isnan(o1)));
+            }
+        }
+        for (int w = 16; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+        if (2 * lane < cols)
+            reinterpret_cast<uint32_t*>(a.out + (((long long)b * a.Tq + i) * a.Hq + head) * a.dv + 64 * half)[lane] =
+                pack_bf16x2(o0 / l, o1 / l);
+    }
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
 window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const Args a)
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
+                   const __grid_constant__ Args a)
 {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -257,7 +350,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int b = blockIdx.y;
     const int n_keys = a.lengths ? min(max(a.lengths[b], 0), a.Tk) : a.Tk;
-    const Plan p = make_plan(a, n_keys);
+    const Plan p = make_plan(a, n_keys, blockIdx.x);
     if (p.n == 0) return;                      // all padding
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gb + kOffAbort);
     auto bar = [&](uint32_t i) { return base + kOffBar + 8u * i; };
@@ -451,11 +544,13 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     for (int e = 0; e < 32; ++e) x[e] = (keep & (1u << e)) ? x[e] : -INFINITY;
                 }
             };
-            // rows of padding in V hold anything: zero times that must be zero
-            if (half == 0 && n_keys - s0 < kBN && n_keys < a.Tk) {
+            // rows of V past what any query of this tile sees (padding; beside the sinks of a tile that is no
+            // window's) hold anything: zero times that must be zero
+            const int v_end = sink_tile ? p.sink : n_keys;
+            if (half == 0 && v_end - s0 < kBN && (sink_tile || n_keys < a.Tk)) {
                 const uint32_t v = base + kOffV + (uint32_t)(j % kVStages) * kOp;
                 if (!wait(bar(kBarVFull + j % kVStages), (uint32_t)(j / kVStages), 49)) break;
-                for (int r = (n_keys - s0) * 8 + row; r < kBN * 8; r += kBM)
+                for (int r = (v_end - s0) * 8 + row; r < kBN * 8; r += kBM)
                     for (int c = 0; c < nbv; ++c) st_shared_v4(v + c * kBox + 16u * r, 0, 0, 0, 0);
                 fence_proxy_async_smem();
             }
@@ -585,6 +680,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const bool cut = p_hi + 1 < a.Tk - a.Tq + min(row0 + kBM, a.Tq);
                 const uint32_t stage = base + kOffQ + q * kOp + half * kBox + (uint32_t)row * 128u;
                 __nv_bfloat16* orow = a.out + (((long long)b * a.Tq + row0 + row) * a.Hq + head) * a.dv + 64 * half;
+                uint64_t zero = 0ull;                         // O times 0: NaN where O is not finite
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     if (c >= groups) break;
@@ -593,7 +689,10 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     tmem_wait_ld();
                     uint32_t w[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+                    for (int e = 0; e < 8; ++e) {
+                        zero = attn::fma2(attn::f2pack(o[2 * e], o[2 * e + 1]), 0ull, zero);
+                        w[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+                    }
                     if (!cut) {
                         st_shared_v4(stage + (uint32_t)(((2 * c) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
                         st_shared_v4(stage + (uint32_t)(((2 * c + 1) ^ (row & 7)) << 4), w[4], w[5], w[6], w[7]);
@@ -603,6 +702,9 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                 }
                 const int first = row0 + 32 * (warp & 3);
+                float z0, z1;
+                attn::f2unpack(zero, z0, z1);
+                const bool redo = __any_sync(0xffffffffu, t <= p_hi && !(z0 + z1 == 0.0f));
                 if (!cut && groups > 0 && first < a.Tq) {
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -613,6 +715,7 @@ window_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     }
                     __syncwarp();
                 }
+                if (redo) redo_rows(a);
             }
         }
     }
@@ -1013,6 +1116,10 @@ cudaError_t launch_window(const WindowArgs& a, cudaStream_t stream)
     cudaError_t e = cudaFuncSetAttribute(window_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e != cudaSuccess) return e;
     Args r;
+    r.q = a.q; r.k = a.k; r.v = a.v;
+    r.q_batch = a.q_batch; r.q_row = a.q_row; r.q_head = a.q_head;
+    r.k_batch = a.k_batch; r.k_row = a.k_row; r.k_head = a.k_head;
+    r.v_batch = a.v_batch; r.v_row = a.v_row; r.v_head = a.v_head;
     r.lengths = a.lengths;
     r.out = a.out;
     r.Tq = a.Tq; r.Tk = a.Tk; r.Hq = a.Hq; r.group = a.Hq / a.Hkv; r.dk = a.dk; r.dv = a.dv;

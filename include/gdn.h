@@ -458,9 +458,8 @@ int gdn_selective_scan_step_f32(const float* x, long long x_batch_stride, const 
  * Hq a multiple of Hkv; d_k, d_v multiples of 16 in 16..128; window >= 1,
  * sinks >= 0, scale > 0 and finite.  Scores and the softmax in fp32, the weights
  * rounded to bf16 for their product with v, out rounded once.  Rows of k and v past
- * a sequence's length may hold anything; a value of v before it that is not finite
- * reaches every query of the 128 computed together, as zero times it does in the
- * formula.
+ * a sequence's length may hold anything; values of k and v that are not finite reach
+ * the queries that see their token and no others.
  */
 int gdn_window_attention(const void* q, long long q_batch_stride, long long q_row_stride, long long q_head_stride,
                          const void* k, long long k_batch_stride, long long k_row_stride, long long k_head_stride,

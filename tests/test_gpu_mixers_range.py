@@ -260,3 +260,63 @@ def test_window_attention_over_the_range_of_values(cuda, size, rise):
     S = 8.0 * 4 * rise / 8.0 + 8.0
     tol = 2.0 ** -8 * (np.abs(ref) + mag) + (2.0 ** -12 + 2 * S * 2.0 ** -20) * mag + 4 * 2.0 ** -133
     assert_near(o[0], ref, tol, "values at the ends of the range")
+
+
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+@pytest.mark.parametrize("Tq,Tk,Hq,Hkv,dv,window,sinks,lengths", [
+    (300, 300, 2, 2, 64, 40, 3, None), (300, 300, 4, 2, 112, 200, 0, None), (700, 700, 3, 1, 128, 150, 40, [700, 650]),
+    (70, 330, 2, 1, 48, 90, 20, None), (33, 33, 2, 2, 16, 1, 0, None),
+])
+def test_unseen_values_stay_unseen(cuda, value, Tq, Tk, Hq, Hkv, dv, window, sinks, lengths):
+    """NaN and infinities in v reach the queries that see their token and no others: not those before it,
+    not those whose window has passed it."""
+    g = gen(114)
+    B = 1 if lengths is None else len(lengths)
+    q, k, v = attn_inputs(g, B, Tq, Tk, Hq, Hkv, 64, dv)
+    at = sorted({Tk - 1, Tk - Tq + Tq // 2, max(0, Tk - Tq - 10), Tk // 3})
+    for i, s in enumerate(at):
+        v[:, s, i % Hkv, (5 * i) % dv] = value
+    v[:, Tk - 3, 0] = value
+    ln = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device=cuda)
+    o = np64(G.window_attention(q, k, v, window, sinks, ln))
+    done()
+    seen = 0
+    for b in range(B):
+        n = Tk if lengths is None else lengths[b]
+        m = min(Tq, n - (Tk - Tq))
+        with np.errstate(invalid="ignore"):
+            ref, mag = M.window_attention(np64(q[b, :m]), np64(k[b, :n]), np64(v[b, :n]), window, sinks)
+        same_kind(o[b, :m], ref, attn_tol(ref, mag), f"values of {value}")
+        seen += int((~np.isfinite(ref)).sum())
+    assert seen
+
+
+@pytest.mark.parametrize("value", [NAN, INF])
+def test_unseen_values_stay_unseen_in_a_step(cuda, value):
+    g = gen(115)
+    q, k, v, kc, vc, pos = step_inputs(g, 2, 4, 2, 64, 30, 4, [20, 12])
+    vc[:, 21:] = value
+    kc[:, 21:] = value
+    vc[1, 13:], kc[1, 13:] = value, value
+    out = G.window_attention_step(q, k, v, kc, vc, pos, 30, 4)
+    done()
+    check_step(q, kc, vc, pos, np64(out), 30, 4, "step beside unused slots")
+
+
+@pytest.mark.parametrize("value", [NAN, INF])
+def test_unseen_keys_stay_unseen(cuda, value):
+    """The same of keys; with NaN in all of v, every row is NaN."""
+    g = gen(119)
+    T, window, sinks = 400, 60, 2
+    q, k, v = attn_inputs(g, 1, T, T, 4, 2, 96, 96)
+    k[0, 50, 0, 3], k[0, 51, 1, 9], k[0, 399, :, 0], v[0, 51, 1, 9] = value, value, value, NAN
+    o = np64(G.window_attention(q, k, v, window, sinks))
+    done()
+    with np.errstate(invalid="ignore"):
+        ref, mag = M.window_attention(np64(q[0]), np64(k[0]), np64(v[0]), window, sinks)
+    for rows in (np.isfinite(ref), np.isnan(ref)):
+        assert rows.any()
+    same_kind(o[0], ref, attn_tol(ref, mag), f"keys of {value}")
+    o = G.window_attention(q, torch.zeros_like(k), torch.full_like(v, NAN), window, sinks)
+    done()
+    assert torch.isnan(o).all()
