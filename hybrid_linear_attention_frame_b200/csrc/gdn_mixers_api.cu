@@ -129,6 +129,44 @@ int check_heads(const void* p, long long* batch, long long* row, long long* head
     return GDN_OK;
 }
 
+int run_window_step(const void* q, long long q_batch_stride, const void* k, long long k_batch_stride,
+                    const void* v, long long v_batch_stride, void* k_cache, void* v_cache,
+                    const int* pos, void* out, int B, int Hq, int Hkv, int d_k, int d_v,
+                    int window, int sinks, float scale, bool zero_idle, cudaStream_t stream)
+{
+    int st = check_window(B, Hq, Hkv, d_k, d_v, window, sinks, scale);
+    if (st != GDN_OK) return st;
+    if ((int64_t)window + sinks > INT32_MAX - 64) return GDN_ERR_UNSUPPORTED;
+    if (!q || !k || !v || !k_cache || !v_cache || !pos || !out) return GDN_ERR_INVALID_ARG;
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) || !aligned(pos, 4))
+        return GDN_ERR_INVALID_ARG;
+    Rows rq{q, q_batch_stride, 0}, rk{k, k_batch_stride, 0}, rv{v, v_batch_stride, 0};
+    size_t nq, nk, nv;
+    st = check_rows(&rq, B, 1, (long long)Hq * d_k, 2, &nq);
+    if (st == GDN_OK) st = check_rows(&rk, B, 1, (long long)Hkv * d_k, 2, &nk);
+    if (st == GDN_OK) st = check_rows(&rv, B, 1, (long long)Hkv * d_v, 2, &nv);
+    if (st != GDN_OK) return st;
+    const size_t slots = (size_t)B * ((size_t)window + sinks) * Hkv, nkc = slots * d_k * 2, nvc = slots * d_v * 2;
+    const size_t no = (size_t)B * Hq * d_v * 2;
+    const Span in[] = {{q, nq}, {k, nk}, {v, nv}, {pos, (size_t)B * 4}};
+    if (overlaps_any(k_cache, nkc, in) || overlaps_any(v_cache, nvc, in) || overlaps(k_cache, nkc, v_cache, nvc) ||
+        overlaps_any(out, no, in) || overlaps(out, no, k_cache, nkc) || overlaps(out, no, v_cache, nvc))
+        return GDN_ERR_INVALID_ARG;
+    gdn::StepArgs a;
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.k = static_cast<const __nv_bfloat16*>(k);
+    a.v = static_cast<const __nv_bfloat16*>(v);
+    a.q_batch = rq.batch; a.k_batch = rk.batch; a.v_batch = rv.batch;
+    a.k_cache = static_cast<__nv_bfloat16*>(k_cache);
+    a.v_cache = static_cast<__nv_bfloat16*>(v_cache);
+    a.pos = pos;
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.dk = d_k; a.dv = d_v; a.window = window; a.sinks = sinks;
+    a.scale = scale;
+    a.zero_idle = zero_idle;
+    return to_status(gdn::launch_window_step(a, stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -289,36 +327,17 @@ int gdn_window_attention_step(const void* q, long long q_batch_stride, const voi
                               const int* pos, void* out, int B, int Hq, int Hkv, int d_k, int d_v,
                               int window, int sinks, float scale, cudaStream_t stream)
 {
-    int st = check_window(B, Hq, Hkv, d_k, d_v, window, sinks, scale);
-    if (st != GDN_OK) return st;
-    if ((int64_t)window + sinks > INT32_MAX - 64) return GDN_ERR_UNSUPPORTED;
-    if (!q || !k || !v || !k_cache || !v_cache || !pos || !out) return GDN_ERR_INVALID_ARG;
-    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) || !aligned(pos, 4))
-        return GDN_ERR_INVALID_ARG;
-    Rows rq{q, q_batch_stride, 0}, rk{k, k_batch_stride, 0}, rv{v, v_batch_stride, 0};
-    size_t nq, nk, nv;
-    st = check_rows(&rq, B, 1, (long long)Hq * d_k, 2, &nq);
-    if (st == GDN_OK) st = check_rows(&rk, B, 1, (long long)Hkv * d_k, 2, &nk);
-    if (st == GDN_OK) st = check_rows(&rv, B, 1, (long long)Hkv * d_v, 2, &nv);
-    if (st != GDN_OK) return st;
-    const size_t slots = (size_t)B * ((size_t)window + sinks) * Hkv, nkc = slots * d_k * 2, nvc = slots * d_v * 2;
-    const size_t no = (size_t)B * Hq * d_v * 2;
-    const Span in[] = {{q, nq}, {k, nk}, {v, nv}, {pos, (size_t)B * 4}};
-    if (overlaps_any(k_cache, nkc, in) || overlaps_any(v_cache, nvc, in) || overlaps(k_cache, nkc, v_cache, nvc) ||
-        overlaps_any(out, no, in) || overlaps(out, no, k_cache, nkc) || overlaps(out, no, v_cache, nvc))
-        return GDN_ERR_INVALID_ARG;
-    gdn::StepArgs a;
-    a.q = static_cast<const __nv_bfloat16*>(q);
-    a.k = static_cast<const __nv_bfloat16*>(k);
-    a.v = static_cast<const __nv_bfloat16*>(v);
-    a.q_batch = rq.batch; a.k_batch = rk.batch; a.v_batch = rv.batch;
-    a.k_cache = static_cast<__nv_bfloat16*>(k_cache);
-    a.v_cache = static_cast<__nv_bfloat16*>(v_cache);
-    a.pos = pos;
-    a.out = static_cast<__nv_bfloat16*>(out);
-    a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.dk = d_k; a.dv = d_v; a.window = window; a.sinks = sinks;
-    a.scale = scale;
-    return to_status(gdn::launch_window_step(a, stream));
+    return run_window_step(q, q_batch_stride, k, k_batch_stride, v, v_batch_stride, k_cache, v_cache, pos, out, B, Hq,
+                           Hkv, d_k, d_v, window, sinks, scale, false, stream);
+}
+
+int gdn_window_attention_step_zero_idle(const void* q, long long q_batch_stride, const void* k, long long k_batch_stride,
+                                        const void* v, long long v_batch_stride, void* k_cache, void* v_cache,
+                                        const int* pos, void* out, int B, int Hq, int Hkv, int d_k, int d_v,
+                                        int window, int sinks, float scale, cudaStream_t stream)
+{
+    return run_window_step(q, q_batch_stride, k, k_batch_stride, v, v_batch_stride, k_cache, v_cache, pos, out, B, Hq,
+                           Hkv, d_k, d_v, window, sinks, scale, true, stream);
 }
 
 }  // extern "C"

@@ -28,10 +28,11 @@ struct StepArgs {
     const __nv_bfloat16 *q, *k, *v;          // [B, Hq, dk], [B, Hkv, dk], [B, Hkv, dv]
     long long q_batch, k_batch, v_batch;
     __nv_bfloat16 *k_cache, *v_cache;        // [B, window + sinks, Hkv, d]
-    const int* pos;                          // [B]: the token's position; negative: nothing is done
+    const int* pos;                          // [B]: the token's position; negative: an idle session
     __nv_bfloat16* out;                      // [B, Hq, dv]
     int B, Hq, Hkv, dk, dv, window, sinks;
     float scale;
+    bool zero_idle;                          // an idle session's row of out: zeros, else as it was
     uint64_t wait_limit_ns;
 };
 
@@ -807,7 +808,12 @@ window_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     }
     fence_mbar_init();
     __syncthreads();
-    if (pos < 0) return;                       // idle: the whole cluster leaves
+    if (pos < 0) {                             // idle: the whole cluster leaves
+        uint4* row = reinterpret_cast<uint4*>(a.out + ((long long)b * a.Hq + hk * G + g0) * a.dv);
+        if (a.zero_idle && rank == 0)
+            for (int i = tid; i < min(kRows, G - g0) * a.dv / 8; i += kThreads) row[i] = make_uint4(0, 0, 0, 0);
+        return;
+    }
     const int cap = a.window + a.sinks;
     const int slot = (int)cache_slot(pos, a.window, a.sinks);
     const int seen = pos + 1 < cap ? (int)(pos + 1) : cap;

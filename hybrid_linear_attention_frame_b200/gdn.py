@@ -27,7 +27,8 @@ EXPORTS = ("gdn_forward", "gdn_state_step", "gdn_forward_f32", "gdn_state_step_f
            "gdn_get_last_device_status", "gdn_bf16_path", "gdn_version",
            "gdn_causal_conv", "gdn_causal_conv_f32", "gdn_causal_conv_step", "gdn_causal_conv_step_f32",
            "gdn_selective_scan", "gdn_selective_scan_f32", "gdn_selective_scan_step", "gdn_selective_scan_step_f32",
-           "gdn_window_attention", "gdn_window_cache_append", "gdn_window_attention_step")
+           "gdn_window_attention", "gdn_window_cache_append", "gdn_window_attention_step",
+           "gdn_window_attention_step_zero_idle")
 
 
 class GdnError(RuntimeError):

@@ -19,6 +19,8 @@ _CONV_STEP = [_P, _L, _P, _P, _P, _P] + [_I] * 4 + [_P]
 _SCAN = [_P, _L, _L] * 2 + [_P] + [_P, _L, _L] * 2 + [_P] + [_P, _L, _L] + [_P] * 5 + [_I] * 5 + [_P]
 _SCAN_STEP = [_P, _L] * 2 + [_P] + [_P, _L] * 2 + [_P, _P, _L] + [_P] * 3 + [_I] * 4 + [_P]
 
+_WINDOW_STEP = [_P, _L] * 3 + [_P] * 4 + [_I] * 7 + [_F, _P]
+
 _ARGTYPES = {
     "gdn_causal_conv": _CONV, "gdn_causal_conv_f32": _CONV,
     "gdn_causal_conv_step": _CONV_STEP, "gdn_causal_conv_step_f32": _CONV_STEP,
@@ -26,7 +28,7 @@ _ARGTYPES = {
     "gdn_selective_scan_step": _SCAN_STEP, "gdn_selective_scan_step_f32": _SCAN_STEP,
     "gdn_window_attention": [_P, _L, _L, _L] * 3 + [_P, _P] + [_I] * 9 + [_F, _P],
     "gdn_window_cache_append": [_P, _L, _L] * 2 + [_P] * 4 + [_I] * 7 + [_P],
-    "gdn_window_attention_step": [_P, _L] * 3 + [_P] * 4 + [_I] * 7 + [_F, _P],
+    "gdn_window_attention_step": _WINDOW_STEP, "gdn_window_attention_step_zero_idle": _WINDOW_STEP,
 }
 
 _fns = {}
@@ -230,8 +232,10 @@ def window_cache_append(k, v, k_cache, v_cache, start, window, sinks=0, lengths=
 
 def window_attention_step(q, k, v, k_cache, v_cache, pos, window, sinks=0, scale=None, out=None):
     """out [B, Hq, d_v] for one token per session: k, v [B, Hkv, d] go into the rolling caches as
-    token pos[b] (int32 [B]; negative: an idle session) and q [B, Hq, d_k] attends over them."""
-    dev, ty, i32 = _bf16(q, "q", "gdn_window_attention_step")
+    token pos[b] (int32 [B]) and q [B, Hq, d_k] attends over them.  pos[b] < 0 marks an idle
+    session: its cache stays, its row of the result is zeros, or as it was when ``out`` is given."""
+    name = "gdn_window_attention_step_zero_idle" if out is None else "gdn_window_attention_step"
+    dev, ty, i32 = _bf16(q, "q", name)
     B, Hq, dk = q.shape
     _, Hkv, dv = v.shape
     qp, qs = _token(q, "q", q.shape, ty, dev)
@@ -241,6 +245,6 @@ def window_attention_step(q, k, v, k_cache, v_cache, pos, window, sinks=0, scale
     vc = _whole(v_cache, "v_cache", (B, window + sinks, Hkv, dv), ty, dev)
     pp = _whole(pos, "pos", (B,), i32, dev)
     out = _new(out, "out", q, (B, Hq, dv), ty)
-    _call("gdn_window_attention_step", dev, qp, qs[0], kp, ks[0], vp, vs[0], kc, vc, pp, out.data_ptr(), B, Hq, Hkv, dk,
+    _call(name, dev, qp, qs[0], kp, ks[0], vp, vs[0], kc, vc, pp, out.data_ptr(), B, Hq, Hkv, dk,
           dv, window, sinks, dk ** -0.5 if scale is None else scale)
     return out

@@ -490,13 +490,18 @@ int gdn_window_cache_append(const void* k, long long k_batch_stride, long long k
  * token pos[b] and writes out [B, Hq, d_v] = the attention of q [B, Hq, d_k] over
  * what that position sees.  pos (device, int32 [B]) counts from 0; the session's
  * tokens before it must be in the cache.  pos[b] < 0 marks an idle session: its
- * cache and its row of out are left as they were.  Heads, sizes and rounding as in
- * gdn_window_attention.
+ * cache and its row of out are left as they were (gdn_window_attention_step_zero_idle:
+ * the row is zeroed).  Heads, sizes and rounding as in gdn_window_attention.
  */
 int gdn_window_attention_step(const void* q, long long q_batch_stride, const void* k, long long k_batch_stride,
                               const void* v, long long v_batch_stride, void* k_cache, void* v_cache,
                               const int* pos, void* out, int B, int Hq, int Hkv, int d_k, int d_v,
                               int window, int sinks, float scale, cudaStream_t stream);
+
+int gdn_window_attention_step_zero_idle(const void* q, long long q_batch_stride, const void* k, long long k_batch_stride,
+                                        const void* v, long long v_batch_stride, void* k_cache, void* v_cache,
+                                        const int* pos, void* out, int B, int Hq, int Hkv, int d_k, int d_v,
+                                        int window, int sinks, float scale, cudaStream_t stream);
 
 /* Human-readable text of a gdn_status value (static storage). */
 const char* gdn_status_string(int status);

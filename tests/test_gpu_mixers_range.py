@@ -320,3 +320,23 @@ def test_unseen_keys_stay_unseen(cuda, value):
     o = G.window_attention(q, torch.zeros_like(k), torch.full_like(v, NAN), window, sinks)
     done()
     assert torch.isnan(o).all()
+
+
+def test_idle_sessions_get_zeros_unless_out_is_given(cuda):
+    """New memory is not handed out as it is: an idle session's row of a new `out` is zero; a given one stays."""
+    g = gen(116)
+    q, k, v, kc, vc, pos = step_inputs(g, 6, 4, 2, 64, 30, 4, [-1, 3, -7, 100, -(2 ** 31), 0])
+    for _ in range(3):
+        junk = torch.full((6, 4, 64), NAN, dtype=torch.bfloat16, device=cuda)
+        del junk                                      # (its memory is the next call's)
+        before = kc.clone(), vc.clone()
+        out = G.window_attention_step(q, k, v, kc, vc, pos, 30, 4)
+        done()
+        idle = pos < 0
+        assert (out[idle] == 0).all() and torch.isfinite(out[~idle]).all() and (out[~idle] != 0).any()
+        assert torch.equal(kc[idle], before[0][idle]) and torch.equal(vc[idle], before[1][idle])
+    given = Guarded((6, 4, 64), torch.bfloat16, 5.0)
+    G.window_attention_step(q, k, v, kc, vc, pos, 30, 4, out=given.t)
+    done()
+    o = given.check()
+    assert (o[idle.cpu().numpy()] == 5.0).all() and np.array_equal(o[~idle.cpu().numpy()], np64(out[~idle]))

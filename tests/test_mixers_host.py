@@ -138,3 +138,10 @@ def test_argument_lists_match_the_header():
                     ctypes.c_longlong if d.startswith("long long") else
                     ctypes.c_float if d.startswith("float") else ctypes.c_int)
             assert t is want, (name, d)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(q=None), INV), (dict(pos=None), INV), (dict(out=at(4) + 64), INV), (dict(window=0), INV), (dict(dv=136), UNS),
+])
+def test_step_with_zeros_for_idle_sessions_refuses(kw, expect):
+    assert entry("gdn_window_attention_step_zero_idle", STEP, **kw) == expect
