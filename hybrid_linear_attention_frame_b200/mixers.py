@@ -65,6 +65,11 @@ def _need(cond, what):
         raise ValueError(what)
 
 
+def _sizes(*n):
+    """ctypes would cut a larger number to its low 32 bits."""
+    _need(-2 ** 31 <= min(n) and max(n) < 2 ** 31, "a size, window or sink count exceeds 32 bits")
+
+
 def _mismatch(t, name, shape, dtype, device):
     raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
@@ -122,6 +127,7 @@ def causal_conv(x, weight, bias=None, state=None, silu=True, lengths=None, out=N
     name, dev, ty, f32, i32 = _types(x, "x", "gdn_causal_conv")
     B, T, D = x.shape
     W = weight.shape[1]
+    _sizes(B, T, D)
     xp, xs = _rows(x, "x", x.shape, ty, dev)
     wp, bp = _whole(weight, "weight", (D, W), f32, dev), _whole(bias, "bias", (D,), f32, dev)
     sp, lp = _whole(state, "state", (B, W - 1, D), ty, dev), _whole(lengths, "lengths", (B,), i32, dev)
@@ -136,6 +142,7 @@ def causal_conv_step(x, weight, bias, state, silu=True, out=None):
     name, dev, ty, f32, _ = _types(x, "x", "gdn_causal_conv_step")
     B, D = x.shape
     W = weight.shape[1]
+    _sizes(B, D)
     xp, xs = _rows(x, "x", x.shape, ty, dev)
     wp, bp = _whole(weight, "weight", (D, W), f32, dev), _whole(bias, "bias", (D,), f32, dev)
     sp = _whole(state, "state", (B, W - 1, D), ty, dev)
@@ -151,6 +158,7 @@ def selective_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, state=None, d
     name, dev, ty, f32, i32 = _types(x, "x", "gdn_selective_scan")
     B, T, E = x.shape
     N = A.shape[1]
+    _sizes(B, T, E)
     xp, xs = _rows(x, "x", x.shape, ty, dev)
     dp, ds = _rows(dt, "dt", x.shape, ty, dev)
     bp, bs = _rows(Bm, "Bm", (B, T, N), ty, dev)
@@ -171,6 +179,7 @@ def selective_scan_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, d
     name, dev, ty, f32, _ = _types(x, "x", "gdn_selective_scan_step")
     B, E = x.shape
     N = A.shape[1]
+    _sizes(B, E)
     xp, xs = _rows(x, "x", x.shape, ty, dev)
     dp, ds = _rows(dt, "dt", x.shape, ty, dev)
     bp, bs = _rows(Bm, "Bm", (B, N), ty, dev)
@@ -191,6 +200,7 @@ def window_attention(q, k, v, window, sinks=0, lengths=None, scale=None, out=Non
     dev, ty, i32 = _bf16(q, "q", "gdn_window_attention")
     B, Tq, Hq, dk = q.shape
     _, Tk, Hkv, dv = v.shape
+    _sizes(B, Tk, Hq, window, sinks)
     qp, qs = _rows(q, "q", q.shape, ty, dev)
     kp, ks = _rows(k, "k", (B, Tk, Hkv, dk), ty, dev)
     vp, vs = _rows(v, "v", (B, Tk, Hkv, dv), ty, dev)
@@ -221,6 +231,7 @@ def window_cache_append(k, v, k_cache, v_cache, start, window, sinks=0, lengths=
     dev, ty, i32 = _bf16(k, "k", "gdn_window_cache_append")
     B, T, Hkv, dk = k.shape
     dv = v.shape[3]
+    _sizes(B, T, Hkv, window, sinks)
     kp, ks = _token(k, "k", k.shape, ty, dev)
     vp, vs = _token(v, "v", (B, T, Hkv, dv), ty, dev)
     kc = _whole(k_cache, "k_cache", (B, window + sinks, Hkv, dk), ty, dev)
@@ -238,6 +249,7 @@ def window_attention_step(q, k, v, k_cache, v_cache, pos, window, sinks=0, scale
     dev, ty, i32 = _bf16(q, "q", name)
     B, Hq, dk = q.shape
     _, Hkv, dv = v.shape
+    _sizes(B, Hq, window, sinks)
     qp, qs = _token(q, "q", q.shape, ty, dev)
     kp, ks = _token(k, "k", (B, Hkv, dk), ty, dev)
     vp, vs = _token(v, "v", (B, Hkv, dv), ty, dev)

@@ -340,3 +340,21 @@ def test_idle_sessions_get_zeros_unless_out_is_given(cuda):
     done()
     o = given.check()
     assert (o[idle.cpu().numpy()] == 5.0).all() and np.array_equal(o[~idle.cpu().numpy()], np64(out[~idle]))
+
+
+def test_sizes_past_an_int_are_refused(cuda):
+    """A window or sink count that a C int cannot hold is refused, not cut to its low bits."""
+    g = gen(117)
+    q, k, v = attn_inputs(g, 1, 20, 20, 2, 2, 64, 64)
+    for kw in (dict(window=2 ** 32 + 5), dict(window=2 ** 31), dict(window=5, sinks=2 ** 32 + 1), dict(window=2 ** 32)):
+        with pytest.raises(ValueError):
+            G.window_attention(q, k, v, **kw)
+    o = G.window_attention(q, k, v, 2 ** 31 - 1, 2 ** 31 - 1)
+    done()
+    assert torch.equal(o, G.window_attention(q, k, v, 20))
+    kc, vc = G.window_cache(1, 2, 64, 64, 8, 2, cuda)
+    with pytest.raises(ValueError):
+        G.window_cache_append(k, v, kc, vc, None, 2 ** 32 + 8, 2 - 2 ** 32)
+    with pytest.raises(ValueError):
+        G.window_attention_step(q[:, 0], k[:, 0], v[:, 0], kc, vc, torch.zeros(1, dtype=torch.int32, device=cuda),
+                                2 ** 32 + 8, 2 - 2 ** 32)
