@@ -69,7 +69,8 @@ int run_conv(gdn::ConvArgs a, int width, int silu, size_t elem, cudaStream_t str
 int run_scan(gdn::ScanArgs a, int softplus, size_t elem, bool step, cudaStream_t stream)
 {
     if (a.B < 1 || a.T < 0 || a.D < 1 || a.N < 1 || (softplus != 0 && softplus != 1)) return GDN_ERR_INVALID_ARG;
-    if ((a.N != 8 && a.N != 16 && a.N != 32 && a.N != 64) || a.D % 8 || a.B > 65535 || a.T > INT32_MAX - 1024)
+    if ((a.N != 8 && a.N != 16 && a.N != 32 && a.N != 64) || a.D % 8 || a.B > 65535 || a.T > INT32_MAX - 1024 ||
+        a.D > INT32_MAX - 1024)
         return GDN_ERR_UNSUPPORTED;
     if (!a.A || (a.T > 0 && (!a.x || !a.dt || !a.Bm || !a.Cm || !a.y))) return GDN_ERR_INVALID_ARG;
     if (!aligned(a.y, 16) || !aligned(a.A, 16) || !aligned(a.state_in, 16) || !aligned(a.state_out, 16) ||

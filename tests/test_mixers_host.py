@@ -145,3 +145,9 @@ def test_argument_lists_match_the_header():
 ])
 def test_step_with_zeros_for_idle_sessions_refuses(kw, expect):
     assert entry("gdn_window_attention_step_zero_idle", STEP, **kw) == expect
+
+
+@pytest.mark.parametrize("name", ["gdn_selective_scan", "gdn_selective_scan_f32"])
+def test_scan_refuses_channels_that_a_rounded_up_int_cannot_count(name):
+    args = dict(SCAN, B=1, T=1, D=2 ** 31 - 8, lengths=None, state_in=None, state_out=None, z=None)
+    assert mixers._fn(name)(*args.values(), None) == UNS
