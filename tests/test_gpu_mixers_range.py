@@ -358,3 +358,43 @@ def test_sizes_past_an_int_are_refused(cuda):
     with pytest.raises(ValueError):
         G.window_attention_step(q[:, 0], k[:, 0], v[:, 0], kc, vc, torch.zeros(1, dtype=torch.int32, device=cuda),
                                 2 ** 32 + 8, 2 - 2 ** 32)
+
+
+def test_calls_repeat_themselves(cuda):
+    """The same bits every time: no result depends on which block or warp comes first."""
+    g = gen(118)
+    p = scan_inputs(g, 1, 1500, 64, 16, torch.bfloat16)
+    q, k, v = attn_inputs(g, 2, 1100, 1100, 8, 2, 128, 128, std=3.0)
+    s = step_inputs(g, 3, 32, 8, 128, 1000, 16, [1015, 4000, 500])
+    q2, k2, v2 = attn_inputs(g, 1, 333, 333, 3, 3, 112, 112, std=8.0)
+
+    def calls():
+        return [*G.selective_scan(p["x"], p["dt"], p["A"], p["Bm"], p["Cm"], p["D"], p["z"], p["dt_bias"], p["state"]),
+                G.window_attention(q, k, v, 300, 20), G.window_attention(q2, k2, v2, 100, 1),
+                G.window_attention_step(*s, 1000, 16)]
+
+    first = calls()
+    others = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    runs = []
+    for i in range(30):
+        with torch.cuda.stream(others[i % 3]):
+            runs.append(calls())
+    done()
+    assert all(torch.equal(a, b) for r in runs for a, b in zip(first, r))
+
+
+def test_a_block_after_the_cache_has_rolled(cuda):
+    """The next block of a session whose earlier tokens are only in the rolling cache: the sinks, the window's
+    last tokens and the block, in order, stand for the whole sequence."""
+    g = gen(120)
+    window, sinks, n, new = 150, 6, 700, 90
+    q, k, v = attn_inputs(g, 1, n + new, n + new, 4, 2, 64, 64)
+    kc, vc = G.window_cache(1, 2, 64, 64, window, sinks, cuda)
+    G.window_cache_append(k[:, :n], v[:, :n], kc, vc, None, window, sinks)
+    order = [*range(sinks), *(M.slot(p, window, sinks) for p in range(n - window, n))]
+    kk, vv = torch.cat([kc[:, order], k[:, n:]], 1), torch.cat([vc[:, order], v[:, n:]], 1)
+    got = np64(G.window_attention(q[:, n:], kk, vv, window, sinks))
+    done()
+    ref, mag = M.window_attention(np64(q[0, n:]), np64(k[0]), np64(v[0]), window, sinks)
+    assert_near(got[0], ref, attn_tol(ref, mag), "a block after the cache")
