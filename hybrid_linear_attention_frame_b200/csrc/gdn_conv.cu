@@ -7,12 +7,13 @@
 //
 // 2 W + 5 operations and two special functions (the SiLU) per element against two elements of
 // traffic: bound by HBM, with the special-function unit busy for 0.7 of that time, so loads and
-// arithmetic have to overlap.  A thread owns 4 channels, few enough that 6 to 8 blocks of 128 threads
-// share an SM (8 channels a thread: 206 us against 108 us), and walks a stretch of tokens with the
+// arithmetic have to overlap.  A thread owns 4 channels, few enough that blocks of 128 threads share an
+// SM, 6 at width 4 to 8 at width 2 in bf16 and 4 to 6 in float32 (8 channels a thread: 206 us against
+// 108 us), and walks a stretch of tokens with the
 // last W - 1 rows in registers; x is read once but for the W - 1 rows of halo per stretch, and the
 // loads of 8 rows are issued before the first is used.  Channels are the fastest thread index, so a
 // warp reads and writes whole lines of a row.
-// 27,280 tokens of 4480 channels, width 4, bf16: 100 us, 4.9 TB/s.
+// 27,280 tokens of 4480 channels, width 4: bf16 99 us, 4.9 TB/s; float32 167 us, 5.9 TB/s.
 #include "gdn_common.cuh"
 #include "gdn_sm100.cuh"
 
@@ -36,8 +37,8 @@ namespace conv {
 constexpr int kThreads = 128;
 // Tokens per thread: long stretches spare halo rows and weight loads, short ones fill the device (27,280
 // tokens of 4480 channels: 103 us in stretches of 64, 132 us of 16; 333 tokens of 1024 channels: 10.3 us
-// and 5.0 us; both before the weights came by vector loads).  Even the shortest is longer than the halo, so that only stretch 0 reads state_in and
-// state_out may be the same memory.
+// and 5.0 us; both before the weights came by vector loads).  Even the shortest is longer than the halo, so
+// that only stretch 0 reads state_in and state_out may be the same memory.
 constexpr int kMaxStretch = 64, kMinStretch = 8;
 constexpr int V = 4;           // channels per thread
 

@@ -77,6 +77,11 @@ bool make_map(CUtensorMap* map, const void* ptr, int d, int H, long long T, int 
 //     than if every weight were at most 1, and the 2^-16 that O may be small by is within what float
 //     has below bf16's smallest values;
 //   P in bf16 over the score columns it came from, O_q += P_q V with P as the A operand.
+// P enters its product in bf16, each weight off by up to 2^-8 of itself, while the row's sum keeps them in
+// f32: outputs are 0.0019 to 0.0023 from the formula (relative, root mean square) where their own rounding to
+// bf16 makes 0.0016.  The remainders in a second bf16 word, as the form for one token has them, would take 32
+// more registers a thread, held until the row's other thread was looked at (18 warps leave 96), and half
+// again the P V products.
 // S and P of a query tile have two buffers of 64 keys, the halves of a 128-key tile and one thread of
 // each row.  Warp 16 issues, half by half, PV_0(j-1) S_0(j) PV_1(j-1) S_1(j); the tensor cores execute
 // in order, so S(j) may overwrite P(j-1) of its half, and while a softmax weighs one half, the other
@@ -84,10 +89,10 @@ bool make_map(CUtensorMap* map, const void* ptr, int d, int H, long long T, int 
 // counted from the window's first key, sink tiles before them when the two do not touch, so no key is
 // visited twice; a tile that a query tile sees nothing of is skipped for it.  Every wait is bounded.
 //
-// A step (two query tiles, 128 keys, d 128) needs 2.0 K cycles of the tensor cores and 1.8 K of the
+// A step (two query tiles, 128 keys, d 128) needs 2.0 K cycles of the tensor cores and as many of the
 // special-function unit; it takes about 3.6 K, the two taking turns at each buffer.  27,280 tokens,
-// 20 heads on 4, d 128, window 2640 + 880 sinks: 892 us, 1,031 TFLOP/s; causal over 8192 tokens, 32
-// heads on 8: 499 us, 1,101 TFLOP/s.  What the form rests on: one thread per row weighing 128 keys held
+// 20 heads on 4, d 128, window 2640 + 880 sinks: 840 to 930 us as the power cap allows, about 1,020
+// TFLOP/s; causal over 8192 tokens, 32 heads on 8: 528 us, 1,040 TFLOP/s.  What the form rests on: one thread per row weighing 128 keys held
 // the chain from scores to weights to scores at 4.2 K cycles; with S and P in one buffer per tile the
 // softmax waited for both products; an issuing thread that sleeps at its barriers adds 300 cycles to
 // every hand-off (1,008 against 972 us).

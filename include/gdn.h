@@ -356,10 +356,10 @@ int gdn_softmax_attention(const void* q, const void* k, const void* v, void* out
  * Common to them.  Element type bf16 (the *_f32 entries: float32); weights and
  * states as declared.  *_stride arguments are in elements, so that an activation
  * may be a slice of a projection's wider rows: row t of batch entry b starts at
- * p + b * batch_stride + t * row_stride, its elements contiguous.  Every tensor's
- * base must be 16-byte aligned and its strides multiples of 16 bytes; a stride
- * over a dimension of size 1 is not looked at.  Outputs, states and caches are
- * contiguous.  `lengths` (device, int32 [B], may be NULL) gives the number of
+ * p + b * batch_stride + t * row_stride, its elements contiguous; row_stride at least
+ * the row's length, batch_stride 0 or more.  Every tensor's base must be 16-byte
+ * aligned and its strides multiples of 16 bytes; a stride over a dimension of size
+ * 1 is not looked at.  Outputs, states and caches are contiguous.  `lengths` (device, int32 [B], may be NULL) gives the number of
  * valid tokens of each sequence of a padded batch, clamped to [0, T]: rows at and
  * past it are not read into any result and their outputs are left as they were.
  * Work goes to `stream`, one kernel launch per call, no workspace, no allocation,
@@ -452,14 +452,19 @@ int gdn_selective_scan_step_f32(const float* x, long long x_batch_stride, const 
  *     K(t) = {s <= t : s > t - window or s < sinks}.
  * Query heads share key heads in order: head h reads key head h / (Hq / Hkv).
  *   q [B, Tq, Hq, d_k], k [B, Tk, Hkv, d_k], v [B, Tk, Hkv, d_v] bf16, each through
- *   batch, row and head strides (so [B, H, T, d] tensors fit too); out
+ *   batch, row and head strides (so [B, H, T, d] tensors fit too), each at least d of
+ *   its tensor; out
  *   [B, Tq, Hq, d_v] bf16.  With `lengths` a query past its sequence's length is
  *   padding: its row of out is left as it was.
  * Hq a multiple of Hkv; d_k, d_v multiples of 16 in 16..128; window >= 1,
  * sinks >= 0, scale > 0 and finite.  Scores and the softmax in fp32, the weights
  * rounded to bf16 for their product with v, out rounded once.  Rows of k and v past
  * a sequence's length may hold anything; values of k and v that are not finite reach
- * the queries that see their token and no others.
+ * the queries that see their token and no others (a call with such values in v takes
+ * longer: rows that were computed beside them are done again one by one).
+ * Only differences of positions and s < sinks count.  So for the next block of a
+ * session of more than window + sinks tokens, k and v may hold the sinks, the last
+ * `window` tokens before the block, and the block, in order (Tk = sinks + window + Tq).
  */
 int gdn_window_attention(const void* q, long long q_batch_stride, long long q_row_stride, long long q_head_stride,
                          const void* k, long long k_batch_stride, long long k_row_stride, long long k_head_stride,
