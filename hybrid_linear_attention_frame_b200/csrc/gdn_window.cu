@@ -92,10 +92,10 @@ bool make_map(CUtensorMap* map, const void* ptr, int d, int H, long long T, int 
 // A step (two query tiles, 128 keys, d 128) needs 2.0 K cycles of the tensor cores and as many of the
 // special-function unit; it takes about 3.6 K, the two taking turns at each buffer.  27,280 tokens,
 // 20 heads on 4, d 128, window 2640 + 880 sinks: 840 to 930 us as the power cap allows, about 1,020
-// TFLOP/s; causal over 8192 tokens, 32 heads on 8: 528 us, 1,040 TFLOP/s.  What the form rests on: one thread per row weighing 128 keys held
-// the chain from scores to weights to scores at 4.2 K cycles; with S and P in one buffer per tile the
-// softmax waited for both products; an issuing thread that sleeps at its barriers adds 300 cycles to
-// every hand-off (1,008 against 972 us).
+// TFLOP/s; causal over 8192 tokens, 32 heads on 8: 528 us, 1,040 TFLOP/s.  What the form rests on: one
+// thread per row weighing 128 keys held the chain from scores to weights to scores at 4.2 K cycles; with
+// S and P in one buffer per tile the softmax waited for both products; an issuing thread that sleeps at
+// its barriers adds 300 cycles to every hand-off (1,008 against 972 us).
 namespace tc {
 
 using namespace sm100;

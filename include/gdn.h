@@ -359,9 +359,10 @@ int gdn_softmax_attention(const void* q, const void* k, const void* v, void* out
  * p + b * batch_stride + t * row_stride, its elements contiguous; row_stride at least
  * the row's length, batch_stride 0 or more.  Every tensor's base must be 16-byte
  * aligned and its strides multiples of 16 bytes; a stride over a dimension of size
- * 1 is not looked at.  Outputs, states and caches are contiguous.  `lengths` (device, int32 [B], may be NULL) gives the number of
- * valid tokens of each sequence of a padded batch, clamped to [0, T]: rows at and
- * past it are not read into any result and their outputs are left as they were.
+ * 1 is not looked at.  Outputs, states and caches are contiguous.  `lengths` (device,
+ * int32 [B], may be NULL) gives the number of valid tokens of each sequence of a
+ * padded batch, clamped to [0, T]: rows at and past it are not read into any result
+ * and their outputs are left as they were.
  * Work goes to `stream`, one kernel launch per call, no workspace, no allocation,
  * no host synchronisation; the calls can be captured into graphs, and calls in
  * flight on several streams share nothing but the caller's buffers.  Arguments
